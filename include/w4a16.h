@@ -212,6 +212,119 @@ w4_status w4_quantize(const void *W_f16, uint32_t *Wq, void *scales_f16, uint8_t
  */
 w4_status w4_read_probe(const void *src, int64_t bytes, uint32_t *xor_out, int64_t blocks, void *stream);
 
+/* Element types of the decoder-step operators below. */
+enum { W4_F32 = 0, W4_BF16 = 1 };
+
+/*
+ * The decoder-step operators: what runs between the linear layers of a draft or verify
+ * step ("When Do Quantized Drafts Help Speculative Decoding?", "Current pilot setup").  As
+ * for the GEMMs, arguments are validated on the host before any HIP call and launches are
+ * asynchronous on `stream`.  Additionally, a call with no rows (M, T or B = 0) returns W4_OK
+ * without touching anything, strides count elements, and the innermost dimension is
+ * contiguous.  Scratch, where a call needs some, is the (device, stream) workspace described
+ * at w4a16_gemm, with the same rules for captured graphs and concurrent streams.
+ *
+ * Residual addition and root-mean-square norm, with the output in the form that the next
+ * linear layer reads:
+ *     r   = T(residual + x)             T: the residual's type; r = x when residual is NULL
+ *     inv = binary32(1 / sqrt(mean_h(r^2) + eps))       mean and root in binary64
+ *     y   = (r * inv) * weight                          two binary32 roundings
+ *   y_bits = 16: y as bfloat16 [M, H] (A of w4a16_gemm and w8a16_gemm); y_scales unused.
+ *   y_bits = 8:  signed bytes [M, H] and float32 scales [M, H/128], symmetric per row and group
+ *                of 128: s = amax / 127, code = clamp(rint(y / s), -127, 127), 0 if s == 0.
+ *   y_bits = 4:  Aq [M, H/8] and A_scales [M, H/128] of w4a4_gemm: bit for bit what a4_quantize
+ *                gives for the 16-bit output.
+ *   x [M, H], residual [M, H]: W4_F32 or W4_BF16 with row strides >= H; weight [H]: either type.
+ *   residual_out [M, H], dense, of the residual's type: r (it may be the residual itself when
+ *   that is dense).  Codes and r are reproducible bit for bit.
+ *   1 <= H <= 32768; H % 128 == 0 for 8- and 4-bit output; eps >= 0.  Arrays are aligned to
+ *   their type (8-bit codes to 8 bytes); H % 8 == 0 with 16-byte aligned rows takes the
+ *   vectorized path.
+ */
+w4_status w4_rms_norm(const void *x, int x_type, int64_t x_stride, const void *residual, int residual_type,
+                      int64_t residual_stride, const void *weight, int weight_type, double eps, void *y, int y_bits,
+                      float *y_scales, void *residual_out, int64_t M, int64_t H, void *stream);
+
+/*
+ * The values that activation codes and scales stand for, float32 [M, K]: code * scale, for
+ * 8-bit codes (as w4_rms_norm writes them) or 4-bit ones (as w4_rms_norm and a4_quantize do).
+ *   codes 8-byte aligned for 8 bits, 4-byte for 4; out 16-byte aligned.  K % 128 == 0.
+ */
+w4_status w4_act_dequantize(const void *codes, const float *scales, float *out, int64_t M, int64_t K, int bits,
+                            void *stream);
+
+/*
+ * The paged key/value cache.  k_cache and v_cache are pools [pages, kv_heads, page_size, D]:
+ *   cache_bits = 16: bfloat16.
+ *   cache_bits = 8:  signed bytes, with k_scale and v_scale float32 [pages, kv_heads, page_size]:
+ *                    s = amax_D / 127, code = clamp(rint(x / s), -127, 127), 0 if s == 0;
+ *                    it stands for code * s.  binary32 steps with IEEE division, ties to even:
+ *                    bit for bit reproducible.
+ * A token's place is its slot, page * page_size + offset (int64).  D is 64 or 128, 1 <= page_size
+ * <= 65536; caches 16-byte aligned.
+ *
+ * w4_kv_write puts the keys and values of T tokens into their slots; a token whose slot lies
+ * outside [0, pages * page_size) is skipped (padding).  Slots must differ from each other.
+ *   k, v: W4_F32 or W4_BF16 [T, kv_heads, D] with token and head strides (slices of a fused qkv
+ *   row are fine); 16-byte aligned rows take the vectorized path.  8-bit caches: k and v finite.
+ * w4_kv_read reads T slots back: k, v [T, kv_heads, D], dense, 16-byte aligned, W4_F32 or W4_BF16;
+ *   a slot outside the pool gives zeros.
+ */
+w4_status w4_kv_write(const void *k, const void *v, int src_type, int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots, void *k_cache,
+                      void *v_cache, float *k_scale, float *v_scale, int cache_bits, int64_t T, int64_t kv_heads,
+                      int64_t D, int64_t pages, int64_t page_size, void *stream);
+w4_status w4_kv_read(const int64_t *slots, const void *k_cache, const void *v_cache, const float *k_scale,
+                     const float *v_scale, int cache_bits, void *k, void *v, int out_type, int64_t T,
+                     int64_t kv_heads, int64_t D, int64_t pages, int64_t page_size, void *stream);
+
+/*
+ * Attention of B sequences' chunks of new tokens over the paged cache, in which the chunks'
+ * own keys and values already are.  Sequence b holds rows q_start[b] .. q_start[b+1]-1 of q
+ * (n of them) and kv_len[b] cached tokens; its token t lies in page block_table[b][t / page_size].
+ * Its new token i sits at position kv_len[b] - n + i and sees the tokens up to that position:
+ *     out = sum_j softmax_j(scale * q . k_j) v_j
+ * A row at a negative position sees nothing and gives 0.  Query heads h*G .. h*G + G-1 read
+ * key/value head h, G = q_heads / kv_heads.
+ *   q: bfloat16 [T, q_heads, D], token and head strides; out: bfloat16 [T, q_heads, D], dense.
+ *   block_table: int32 [B, table_width], row stride table_stride; q_start: int32 [B+1]; kv_len:
+ *   int32 [B], all on the device.  Rows of q that no chunk holds are not written.
+ *   max_q: no chunk is longer (rows past it are not computed); max_kv: about the longest kv_len,
+ *   which only plans the launch.
+ *   A page number outside [0, pages), or a token past the table's width, gives NaN in the rows
+ *   that see such a token, and never an access outside the pool.
+ *   What the caches hold past a sequence's end does not matter.
+ *   page_size: a multiple of 16 up to 4096.  Scores, softmax and sums are float32; the weights
+ *   are rounded to bfloat16 for the matrix cores.  Bitwise reproducible.
+ */
+w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+                             const void *v_cache, const float *k_scale, const float *v_scale, int cache_bits,
+                             const int32_t *block_table, int64_t table_stride, int64_t table_width,
+                             const int32_t *q_start, const int32_t *kv_len, void *out, float scale, int64_t T,
+                             int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t pages,
+                             int64_t page_size, int64_t max_q, int64_t max_kv, void *stream);
+
+/*
+ * Draws one token a row, from uniform numbers u in [0, 1).  With the tokens of a row ordered
+ * by (logit descending, index ascending) and w_i = exp((logit_i - max) / T):
+ *     keep the first top_k (all, if top_k <= 0);
+ *     of these the shortest prefix whose weights sum to at least top_p times theirs, and at
+ *       least one token (all, if top_p >= 1);
+ *     of these the ones with w_i >= min_p (all, if min_p <= 0; above 1 it counts as 1);
+ *     token = the first index, in the order of the vocabulary, at which the running sum of
+ *       the kept weights passes u times their sum;  prob = w_token / that sum.
+ * temperature <= 0 takes the largest logit (the lowest index of equal ones), prob 1.  A NaN
+ * logit counts as -infinity; a row with nothing above -infinity gives token -1, prob 0.  Weights
+ * are binary64, their sums integers in units of 2^-44 of the largest weight: reproducible bit
+ * for bit, and tokens more than 32 T below the largest logit are never drawn.
+ *   logits: W4_F32 or W4_BF16 [B, V], row stride >= V; 1 <= V <= 2^19, B <= 65535.
+ *   u [B]; temperature, top_k, top_p, min_p: [B] or NULL (1, 0, 1, 0); token: int32 [B]; prob:
+ *   float32 [B] or NULL.
+ */
+w4_status w4_sample(const void *logits, int logits_type, int64_t row_stride, const float *u, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *prob,
+                    int64_t B, int64_t V, void *stream);
+
 /* How w4a16_gemm would run a shape (host only, no HIP call). */
 typedef struct w4_plan {
     int kernel;             /* 1 = small-M wide (4 waves per workgroup, fp16 MFMA),

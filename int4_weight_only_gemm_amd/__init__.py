@@ -9,6 +9,14 @@ package fails loudly when the library has not been built (there is no fallback).
     C = w4.gemm(A_bf16, Wq, s_f16, z_u8)  # [M, N] float32
     Wq8 = w4.pack(q_u8, bits=8)           # 8-bit codes -> [K/4, N] int32 words
     C = w4.gemm(A_bf16, Wq8, s_f16, z_u8, bits=8)
+
+and what runs between the linear layers of a decoder's step:
+
+    A, res = w4.rms_norm(C, weight, residual=res)             # the next product's activations
+    w4.kv_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    o = w4.paged_attention(q, k_cache, v_cache, block_table, q_start, kv_len, max_q, max_kv,
+                           k_scale, v_scale)
+    token, prob = w4.sample(logits, u, temperature=t, top_k=k, top_p=p)
 """
 from __future__ import annotations
 
@@ -75,6 +83,9 @@ class Plan(ctypes.Structure):
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
+_int = ctypes.c_int
+_f32 = ctypes.c_float
+_f64 = ctypes.c_double
 _lib.w4a16_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 _lib.w4a16_gemm.restype = ctypes.c_int
 _lib.w4a16_gemm_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
@@ -99,6 +110,19 @@ _lib.w4a4_plan.argtypes = [_i64, _i64, _i64, ctypes.POINTER(Plan)]
 _lib.w4a4_plan.restype = ctypes.c_int
 _lib.a4_quantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp]
 _lib.a4_quantize.restype = ctypes.c_int
+_lib.w4_rms_norm.argtypes = [_vp, _int, _i64, _vp, _int, _i64, _vp, _int, _f64, _vp, _int, _vp, _vp, _i64, _i64, _vp]
+_lib.w4_rms_norm.restype = ctypes.c_int
+_lib.w4_act_dequantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _int, _vp]
+_lib.w4_act_dequantize.restype = ctypes.c_int
+_lib.w4_kv_write.argtypes = [_vp, _vp, _int] + [_i64] * 4 + [_vp] * 5 + [_int] + [_i64] * 5 + [_vp]
+_lib.w4_kv_write.restype = ctypes.c_int
+_lib.w4_kv_read.argtypes = [_vp] * 5 + [_int, _vp, _vp, _int] + [_i64] * 5 + [_vp]
+_lib.w4_kv_read.restype = ctypes.c_int
+_lib.w4_paged_attention.argtypes = ([_vp, _i64, _i64] + [_vp] * 4 + [_int, _vp, _i64, _i64] + [_vp] * 3 + [_f32]
+                                    + [_i64] * 9 + [_vp])
+_lib.w4_paged_attention.restype = ctypes.c_int
+_lib.w4_sample.argtypes = [_vp, _int, _i64] + [_vp] * 7 + [_i64, _i64, _vp]
+_lib.w4_sample.restype = ctypes.c_int
 _lib.w4_status_string.argtypes = [ctypes.c_int]
 _lib.w4_status_string.restype = ctypes.c_char_p
 _lib.w4_last_error.argtypes = []
@@ -321,3 +345,244 @@ def read_probe_raw(src_ptr: int, nbytes: int, out_ptr: int, blocks: int, stream_
     rc = _lib.w4_read_probe(src_ptr, nbytes, out_ptr, blocks, stream_handle)
     if rc:
         raise W4Error(rc, "w4_read_probe")
+
+
+# ------------------------------------------------------------------------------------
+# The decoder-step operators: residual + RMS norm, the paged key/value cache, attention over
+# it, sampling.  Strides other than the innermost one are free where noted.
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _typed(t, name, ndim) -> int:
+    """Type number of a device tensor of float32 or bfloat16 whose innermost dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    if t.dim() != ndim or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be {ndim}-d with a contiguous last dimension")
+    return kind
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, bits: int = 16, residual_out=None, stream=None):
+    """Residual addition and RMS norm: y = r / sqrt(mean(r^2) + eps) * weight with r = residual + x.
+
+    x: float32 or bfloat16 [M, H] (a gemm's output, any row stride); residual: either type
+    [M, H], or None; weight: either type [H]. Returns, by `bits`,
+      16: y bfloat16 [M, H] (gemm's A);
+       8: (codes int8 [M, H], scales float32 [M, H/128]);
+       4: (Aq int32 [M, H/8], A_scales float32 [M, H/128]) (gemm_a4's activations);
+    and with a residual the new residual r in its type behind them: (y, r) or (codes, scales, r).
+    residual_out: where to put r (the residual itself adds in place); new by default.
+    """
+    xt = _typed(x, "x", 2)
+    M, H = x.shape
+    wt = _typed(weight, "weight", 1)
+    if weight.shape[0] != H:
+        raise ValueError(f"weight must be [{H}]")
+    rt, rs, r_ptr, o_ptr = 0, H, None, None
+    if residual is not None:
+        rt = _typed(residual, "residual", 2)
+        if residual.shape != x.shape:
+            raise ValueError("residual has another shape than x")
+        if residual_out is None:
+            residual_out = torch.empty((M, H), dtype=residual.dtype, device=x.device)
+        else:
+            _check(residual_out, "residual_out", residual.dtype, 2)
+            if residual_out.shape != x.shape:
+                raise ValueError("residual_out has another shape than x")
+        rs, r_ptr, o_ptr = _row_stride(residual), residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    scales, s_ptr = None, None
+    if bits == 16:
+        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    elif bits == 8 or bits == 4:
+        y = torch.empty((M, H) if bits == 8 else (M, H // 8), dtype=torch.int8 if bits == 8 else torch.int32,
+                        device=x.device)
+        scales = torch.empty((M, H // 128), dtype=torch.float32, device=x.device)
+        s_ptr = scales.data_ptr()
+    else:
+        raise ValueError("bits must be 16, 8 or 4")
+    rc = _lib.w4_rms_norm(x.data_ptr(), xt, _row_stride(x), r_ptr, rt, rs, weight.data_ptr(), wt, eps, y.data_ptr(),
+                          bits, s_ptr, o_ptr, M, H, _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_rms_norm")
+    if bits == 16:
+        return y if residual is None else (y, residual_out)
+    return (y, scales) if residual is None else (y, scales, residual_out)
+
+
+def dequantize_activations(codes, scales, bits: int = 4, out=None, stream=None):
+    """The float32 [M, K] values of activation codes: int8 [M, K] (bits = 8) or int32 [M, K/8] (bits = 4,
+    from quantize_activations or rms_norm) times their scales [M, K/128]."""
+    if bits == 8:
+        _check(codes, "codes", torch.int8, 2)
+        M, K = codes.shape
+    elif bits == 4:
+        if codes.dtype not in (torch.int32, torch.uint32):
+            raise TypeError("codes must be int32 or uint32")
+        _check(codes, "codes", codes.dtype, 2)
+        M, K = codes.shape[0], codes.shape[1] * 8
+    else:
+        raise ValueError("bits must be 8 or 4")
+    _check(scales, "scales", torch.float32, 2)
+    if tuple(scales.shape) != (M, K // 128):
+        raise ValueError(f"scales must be [{M}, {K // 128}]")
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.float32, device=codes.device)
+    else:
+        _check(out, "out", torch.float32, 2)
+        if tuple(out.shape) != (M, K):
+            raise ValueError("out has the wrong shape")
+    rc = _lib.w4_act_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), M, K, bits, _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_act_dequantize")
+    return out
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale):
+    """Bits of a cache (16 or 8) and its scales' pointers."""
+    kind = k_cache.dtype
+    if kind not in (torch.bfloat16, torch.int8):
+        raise TypeError(f"k_cache must be bfloat16 or int8 (got {kind})")
+    _check(k_cache, "k_cache", kind, 4)
+    _check(v_cache, "v_cache", kind, 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache have different shapes")
+    if kind == torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        return 16, None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError("an int8 cache needs k_scale and v_scale")
+    _check(k_scale, "k_scale", torch.float32, 3)
+    _check(v_scale, "v_scale", torch.float32, 3)
+    if k_scale.shape != k_cache.shape[:3] or v_scale.shape != k_cache.shape[:3]:
+        raise ValueError("k_scale and v_scale must be [pages, kv_heads, page_size]")
+    return 8, k_scale.data_ptr(), v_scale.data_ptr()
+
+
+def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=None) -> None:
+    """Write the keys and values of new tokens into their slots of the paged cache, quantizing
+    for an int8 cache.
+
+    k, v: float32 or bfloat16 [T, kv_heads, D], any token and head strides; slots: int64 [T],
+    page * page_size + offset (outside the pool: skipped); k_cache, v_cache: bfloat16 or int8
+    [pages, kv_heads, page_size, D]; k_scale, v_scale: float32 [pages, kv_heads, page_size] (int8).
+    """
+    bits, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    kind = _typed(k, "k", 3)
+    if _typed(v, "v", 3) != kind:
+        raise TypeError("k and v have different types")
+    _check(slots, "slots", torch.int64, 1)
+    T, heads, D = k.shape
+    pages, cache_heads, page_size, cache_d = k_cache.shape
+    if v.shape != k.shape or slots.shape[0] != T or cache_heads != heads or cache_d != D:
+        raise ValueError(f"inconsistent shapes k{tuple(k.shape)} v{tuple(v.shape)} slots{tuple(slots.shape)} "
+                         f"k_cache{tuple(k_cache.shape)}")
+    rc = _lib.w4_kv_write(k.data_ptr(), v.data_ptr(), kind, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                          slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bits, T, heads, D, pages,
+                          page_size, _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_kv_write")
+
+
+def kv_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=torch.bfloat16, stream=None):
+    """Read slots of the paged cache back: (k, v), bfloat16 or float32 [T, kv_heads, D] (zeros for a
+    slot outside the pool)."""
+    bits, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    _check(slots, "slots", torch.int64, 1)
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
+    T = slots.shape[0]
+    pages, heads, page_size, D = k_cache.shape
+    k = torch.empty((T, heads, D), dtype=dtype, device=k_cache.device)
+    v = torch.empty((T, heads, D), dtype=dtype, device=k_cache.device)
+    rc = _lib.w4_kv_read(slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bits, k.data_ptr(),
+                         v.data_ptr(), _TYPES[dtype], T, heads, D, pages, page_size, _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_kv_read")
+    return k, v
+
+
+def paged_attention(q, k_cache, v_cache, block_table, q_start, kv_len, max_q: int, max_kv: int, k_scale=None,
+                    v_scale=None, scale=None, out=None, stream=None):
+    """Attention of chunks of new tokens over the paged cache that already holds them.
+
+    q: bfloat16 [T, q_heads, D], any token and head strides, the sequences' chunks one behind the
+    other: sequence b's rows are q_start[b] .. q_start[b+1]-1 (int32 [B+1]); kv_len: int32 [B] cached
+    tokens, the new ones among them; block_table: int32 [B, width] page numbers (any row stride).
+    New token i of n sees the tokens up to position kv_len - n + i. max_q: the longest chunk;
+    max_kv: the longest sequence (a planning hint). scale: 1/sqrt(D) by default.
+    Returns bfloat16 [T, q_heads, D].
+    """
+    bits, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    if _typed(q, "q", 3) != 1:
+        raise TypeError("q must be bfloat16")
+    T, heads, D = q.shape
+    pages, kv_heads, page_size, cache_d = k_cache.shape
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if block_table.device.type != "cuda" or block_table.dim() != 2 or (block_table.shape[1] > 1
+                                                                       and block_table.stride(1) != 1):
+        raise ValueError("block_table must be a 2-d device tensor with a contiguous last dimension")
+    B, width = block_table.shape
+    _check(q_start, "q_start", torch.int32, 1)
+    _check(kv_len, "kv_len", torch.int32, 1)
+    if cache_d != D or heads % kv_heads or q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
+        raise ValueError(f"inconsistent shapes q{tuple(q.shape)} k_cache{tuple(k_cache.shape)} "
+                         f"block_table{tuple(block_table.shape)} q_start{tuple(q_start.shape)} "
+                         f"kv_len{tuple(kv_len.shape)}")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError("out has the wrong shape")
+    rc = _lib.w4_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+                                 bits, block_table.data_ptr(), block_table.stride(0) if B > 1 else width, width,
+                                 q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+                                 D ** -0.5 if scale is None else scale, T, B, heads, kv_heads, D, pages, page_size,
+                                 max_q, max_kv, _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_paged_attention")
+    return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """Draw one token a row: (token int32 [B], prob float32 [B]).
+
+    logits: float32 or bfloat16 [B, V], any row stride; u: float32 [B] uniform in [0, 1). temperature,
+    top_p, min_p: float32 [B] or None; top_k: int32 [B] or None. Top-k, then top-p of what it
+    keeps, then min-p; temperature <= 0 takes the largest logit. prob is the token's share of the
+    kept weight. A row without a finite logit gives token -1.
+    """
+    kind = _typed(logits, "logits", 2)
+    B, V = logits.shape
+    ptrs = []
+    for t, name, dtype in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
+                           (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                           (min_p, "min_p", torch.float32)):
+        if t is None and name != "u":
+            ptrs.append(None)
+            continue
+        _check(t, name, dtype, 1)
+        if t.shape[0] != B:
+            raise ValueError(f"{name} must be [{B}]")
+        ptrs.append(t.data_ptr())
+    token = torch.empty(B, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(B, dtype=torch.float32, device=logits.device)
+    rc = _lib.w4_sample(logits.data_ptr(), kind, _row_stride(logits), *ptrs, token.data_ptr(), prob.data_ptr(), B, V,
+                        _stream_handle(stream))
+    if rc:
+        raise W4Error(rc, "w4_sample")
+    return token, prob

@@ -5,15 +5,18 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCE = os.path.join(HERE, "csrc", "w4a16.hip")
+SOURCES = [os.path.join(HERE, "csrc", name) for name in ("w4a16.hip", "paged_attention.hip", "sample.hip",
+                                                     "rms_norm.hip", "kv_cache.hip")]
 OUT = os.path.join(HERE, "libw4a16.so")
 ARCH = "gfx950"
 
 FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-Wall", "-Wno-unused-function",
     # packed fp32 VALU ops stay off on this target
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -31,15 +34,28 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = OUT + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), SOURCE, "-o", tmp]
+def _run(cmd) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("hipcc failed to build libw4a16.so")
+    return res.stdout + res.stderr
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles the sources side by side, links them, and puts the library in place."""
+    tmp = OUT + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory() as objects:
+        def compile_one(source: str):
+            obj = os.path.join(objects, os.path.basename(source) + ".o")
+            return obj, _run([hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", source, "-o", obj])
+
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            done = list(pool.map(compile_one, SOURCES))
+        text = "".join(log for _, log in done)
+        text += _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *[obj for obj, _ in done], "-o", tmp])
     if verbose:
-        lines = [l for l in (res.stdout + res.stderr).splitlines() if "not a recognized feature" not in l]
+        lines = [l for l in text.splitlines() if "not a recognized feature" not in l]
         if lines:
             print("\n".join(lines))
     os.replace(tmp, OUT)

@@ -1,0 +1,117 @@
+// internal.h -- what the library's sources share: error text, argument and device checks,
+// the per-(device, stream) workspace, and small device helpers.
+#ifndef W4A16_INTERNAL_H
+#define W4A16_INTERNAL_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+#include <type_traits>
+
+#include "w4a16.h"
+
+#define W4_HIDDEN __attribute__((visibility("hidden")))
+
+namespace w4host {
+
+// Sets the calling thread's w4_last_error() text.
+W4_HIDDEN void set_error(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
+W4_HIDDEN bool aligned(const void *p, uintptr_t a);
+// Sets the error text from a failed HIP call; returns W4_ERR_HIP.
+W4_HIDDEN w4_status hip_fail(const char *what, hipError_t e);
+// W4_OK when the current device is gfx950 (its index in *dev_out).
+W4_HIDDEN w4_status check_device(int *dev_out);
+// The workspace of (dev, stream): `tiles` arrival counters, zero whenever no call is in
+// flight, and `part_bytes` of scratch, 256-byte aligned.  Grows outside stream capture only.
+W4_HIDDEN w4_status get_workspace(int dev, hipStream_t stream, size_t tiles, size_t part_bytes, unsigned **count,
+                                  float **part);
+
+}  // namespace w4host
+
+// ------------------------------------------------------------------------------------
+// Device helpers
+
+namespace w4dev {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+// Two floats rounded to bfloat16 (nearest, ties to even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const bf16x2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ float round_bf16(float a) { return (float)(__bf16)a; }
+
+// Eight consecutive values in registers as they were loaded: 8 bfloat16 in `a`, or 8 floats.
+struct Raw8 {
+    u32x4 a, b;
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t elem)
+{
+    Raw8 r;
+    if (F32) {
+        r.a = *(const u32x4 *)((const float *)p + elem);
+        r.b = *(const u32x4 *)((const float *)p + elem + 4);
+    } else {
+        r.a = *(const u32x4 *)((const uint16_t *)p + elem);
+        r.b = u32x4{0u, 0u, 0u, 0u};
+    }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void raw8_to_float(const Raw8 &r, float (&f)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (F32) {
+            f[j] = __builtin_bit_cast(float, (uint32_t)r.a[j]);
+            f[4 + j] = __builtin_bit_cast(float, (uint32_t)r.b[j]);
+        } else {
+            f[2 * j] = bf16_lo(r.a[j]);
+            f[2 * j + 1] = bf16_hi(r.a[j]);
+        }
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ float load_one(const void *p, int64_t elem)
+{
+    if (F32) return ((const float *)p)[elem];
+    return __builtin_bit_cast(float, (uint32_t)((const uint16_t *)p)[elem] << 16);
+}
+
+// Largest of the 16 lanes of a DPP row, in every lane (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float row16_fmax(float v)
+{
+    auto turn = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x),
+                                                                     decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x128>{}));
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x124>{}));
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x122>{}));
+    return fmaxf(v, turn(v, std::integral_constant<int, 0x121>{}));
+}
+
+// Symmetric code of x on a grid of step s: rint(x / s) within [lo, hi], IEEE division and
+// ties to even, 0 for an empty grid.
+__device__ __forceinline__ int symmetric_code(float x, float s, float lo, float hi)
+{
+    return s == 0.0f ? 0 : (int)fminf(fmaxf(rintf(x / s), lo), hi);
+}
+
+}  // namespace w4dev
+
+#endif  // W4A16_INTERNAL_H

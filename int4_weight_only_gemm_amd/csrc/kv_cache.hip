@@ -1,0 +1,258 @@
+// kv_cache.hip -- the paged key/value cache of a speculative decoder: written quantized as the
+// keys and values of new tokens arrive, and read back, for gfx950.
+//
+// Layout: k_cache and v_cache [pages, kv_heads, page_size, D], so that one head's tokens of a
+// page are one contiguous block (the attention of a head streams it).  16-bit caches hold
+// bfloat16; 8-bit caches hold signed codes with a float32 scale per token and head,
+// [pages, kv_heads, page_size]:
+//     s = amax / 127,  code = clamp(rint(x / s), -127, 127)  (0 if s == 0),  value = code * s
+// every step in binary32 with IEEE division and ties to even, so codes and values are
+// reproducible bit for bit.  One scale per token and head keeps a token's write independent of
+// its neighbours (no requantizing as a page fills).
+//
+// A token's place is its slot, page * page_size + offset; a slot outside the pool is skipped by
+// the write and read back as zeros (padding tokens carry -1).
+#include "internal.h"
+
+using namespace w4host;
+using namespace w4dev;
+
+namespace {
+
+struct KvParams {
+    const void *src[2];   // new keys, new values (write)
+    void *cache[2];
+    float *scale[2];
+    void *dst[2];         // read-back keys, values
+    const int64_t *slots;
+    int64_t tok_stride[2], head_stride[2];
+    int64_t T, pool;      // tokens; slots in the pool
+    int heads, page_size, kind_f32;
+};
+
+// Tokens a workgroup covers for one head and one of the two caches: 16 lanes (D = 128) or
+// 8 lanes (D = 64) hold a token's row, 8 values each.
+template <int D>
+constexpr int kTokens = 256 / (D / 8);
+
+// The place of a slot: first element of its row, and its scale's index.  The pool may pass
+// 2^31 elements: 64-bit throughout.
+template <int D>
+__device__ __forceinline__ int64_t row_of(int64_t slot, int head, int heads, int page_size)
+{
+    const int64_t page = slot / page_size;
+    return (page * heads + head) * page_size + (slot - page * page_size);
+}
+
+template <int D, bool BITS8, bool F32, bool VEC>
+__global__ __launch_bounds__(256) void kv_write_kernel(const KvParams p)
+{
+    constexpr int kLanes = D / 8;
+    const int head = blockIdx.y, which = blockIdx.z;
+    const int64_t t = (int64_t)blockIdx.x * kTokens<D> + threadIdx.x / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const int64_t slot = t < p.T ? p.slots[t] : -1;
+    const bool live = slot >= 0 && slot < p.pool;
+    float f[8];
+    const int64_t at = live ? t * p.tok_stride[which] + head * p.head_stride[which] + lane * 8 : 0;
+    if constexpr (VEC) {
+        raw8_to_float<F32>(load_raw8<F32>(p.src[which], at), f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = load_one<F32>(p.src[which], at + (live ? j : 0));
+    }
+    const int64_t row = live ? row_of<D>(slot, head, p.heads, p.page_size) : 0;
+    if constexpr (!BITS8) {
+        if (live)
+            *(u32x4 *)((uint16_t *)p.cache[which] + row * D + lane * 8) =
+                u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+        return;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+    if constexpr (kLanes == 16) {
+        top = row16_fmax(top);
+    } else {
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    }
+    const float s = top / 127.0f;
+    u32x2 word = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        word[j >> 2] |= (uint32_t)(symmetric_code(f[j], s, -127.f, 127.f) & 0xFF) << (8 * (j & 3));
+    if (!live) return;
+    *(u32x2 *)((uint8_t *)p.cache[which] + row * D + lane * 8) = word;
+    if (lane == 0) p.scale[which][row] = s;
+}
+
+template <int D, bool BITS8, bool F32>
+__global__ __launch_bounds__(256) void kv_read_kernel(const KvParams p)
+{
+    constexpr int kLanes = D / 8;
+    const int head = blockIdx.y, which = blockIdx.z;
+    const int64_t t = (int64_t)blockIdx.x * kTokens<D> + threadIdx.x / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    if (t >= p.T) return;
+    const int64_t slot = p.slots[t];
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0 && slot < p.pool) {
+        const int64_t row = row_of<D>(slot, head, p.heads, p.page_size);
+        if constexpr (BITS8) {
+            const u32x2 w = *(const u32x2 *)((const uint8_t *)p.cache[which] + row * D + lane * 8);
+            const float s = p.scale[which][row];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = (float)(int8_t)(w[j >> 2] >> (8 * (j & 3))) * s;
+        } else {
+            raw8_to_float<false>(load_raw8<false>(p.cache[which], row * D + lane * 8), f);
+        }
+    }
+    const int64_t out = (t * p.heads + head) * D + lane * 8;
+    if constexpr (F32) {
+        f32x4 *dst = (f32x4 *)((float *)p.dst[which] + out);
+        dst[0] = f32x4{f[0], f[1], f[2], f[3]};
+        dst[1] = f32x4{f[4], f[5], f[6], f[7]};
+    } else {
+        *(u32x4 *)((uint16_t *)p.dst[which] + out) =
+            u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+    }
+}
+
+// What both entry points ask of the cache's description; `name` for the error text.
+w4_status check_cache(const char *name, int64_t T, int64_t heads, int64_t D, int64_t pages, int64_t page_size,
+                      int cache_bits)
+{
+    if (cache_bits != 16 && cache_bits != 8) {
+        set_error("%s: cache_bits=%d: need 16 or 8", name, cache_bits);
+        return W4_ERR_SHAPE;
+    }
+    if (T < 0 || T > 0x7FFFFFFF || heads < 1 || heads > 65535 || (D != 64 && D != 128) || pages < 1 ||
+        page_size < 1 || page_size > 65536 || pages > ((int64_t)1 << 40) / (heads * page_size * D)) {
+        set_error("%s: T=%lld heads=%lld D=%lld pages=%lld page_size=%lld: need T>=0, 1<=heads<=65535, D 64 or 128, "
+                  "pages>=1, 1<=page_size<=65536", name, (long long)T, (long long)heads, (long long)D,
+                  (long long)pages, (long long)page_size);
+        return W4_ERR_SHAPE;
+    }
+    return W4_OK;
+}
+
+template <int D, bool BITS8>
+void launch_write(const KvParams &p, bool f32, bool vec, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((p.T + kTokens<D> - 1) / kTokens<D>), (unsigned)p.heads, 2), block(256);
+    if (f32 && vec)
+        hipLaunchKernelGGL((kv_write_kernel<D, BITS8, true, true>), grid, block, 0, stream, p);
+    else if (f32)
+        hipLaunchKernelGGL((kv_write_kernel<D, BITS8, true, false>), grid, block, 0, stream, p);
+    else if (vec)
+        hipLaunchKernelGGL((kv_write_kernel<D, BITS8, false, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((kv_write_kernel<D, BITS8, false, false>), grid, block, 0, stream, p);
+}
+
+template <int D, bool BITS8>
+void launch_read(const KvParams &p, bool f32, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((p.T + kTokens<D> - 1) / kTokens<D>), (unsigned)p.heads, 2), block(256);
+    if (f32)
+        hipLaunchKernelGGL((kv_read_kernel<D, BITS8, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((kv_read_kernel<D, BITS8, false>), grid, block, 0, stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+w4_status w4_kv_write(const void *k, const void *v, int src_type, int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots, void *k_cache,
+                      void *v_cache, float *k_scale, float *v_scale, int cache_bits, int64_t T, int64_t kv_heads,
+                      int64_t D, int64_t pages, int64_t page_size, void *stream)
+{
+    w4_status st = check_cache("w4_kv_write", T, kv_heads, D, pages, page_size, cache_bits);
+    if (st != W4_OK) return st;
+    if (src_type != W4_F32 && src_type != W4_BF16) {
+        set_error("w4_kv_write: src_type is neither W4_F32 nor W4_BF16");
+        return W4_ERR_SHAPE;
+    }
+    const int64_t lim = (int64_t)1 << 32;
+    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+        if (s < 0 || s > lim) {
+            set_error("w4_kv_write: a stride is negative or above 2^32");
+            return W4_ERR_SHAPE;
+        }
+    if (T == 0) return W4_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache || (cache_bits == 8 && (!k_scale || !v_scale))) {
+        set_error("w4_kv_write: a required pointer is NULL");
+        return W4_ERR_NULL;
+    }
+    const int size = src_type == W4_F32 ? 4 : 2;
+    if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 8) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        (cache_bits == 8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))) {
+        set_error("w4_kv_write: k and v must be aligned to their type, slots to 8 bytes, the caches to 16, scales to 4");
+        return W4_ERR_ALIGN;
+    }
+    int dev = -1;
+    st = check_device(&dev);
+    if (st != W4_OK) return st;
+    KvParams p = {};
+    p.src[0] = k, p.src[1] = v, p.cache[0] = k_cache, p.cache[1] = v_cache, p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.slots = slots, p.tok_stride[0] = k_token_stride, p.tok_stride[1] = v_token_stride;
+    p.head_stride[0] = k_head_stride, p.head_stride[1] = v_head_stride;
+    p.T = T, p.pool = pages * page_size, p.heads = (int)kv_heads, p.page_size = (int)page_size;
+    const bool vec = aligned(k, 16) && aligned(v, 16) && k_token_stride * size % 16 == 0 &&
+                     k_head_stride * size % 16 == 0 && v_token_stride * size % 16 == 0 && v_head_stride * size % 16 == 0;
+    const bool f32 = src_type == W4_F32;
+    if (D == 128)
+        cache_bits == 8 ? launch_write<128, true>(p, f32, vec, (hipStream_t)stream)
+                        : launch_write<128, false>(p, f32, vec, (hipStream_t)stream);
+    else
+        cache_bits == 8 ? launch_write<64, true>(p, f32, vec, (hipStream_t)stream)
+                        : launch_write<64, false>(p, f32, vec, (hipStream_t)stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("w4_kv_write launch", e);
+    return W4_OK;
+}
+
+w4_status w4_kv_read(const int64_t *slots, const void *k_cache, const void *v_cache, const float *k_scale,
+                     const float *v_scale, int cache_bits, void *k, void *v, int out_type, int64_t T,
+                     int64_t kv_heads, int64_t D, int64_t pages, int64_t page_size, void *stream)
+{
+    w4_status st = check_cache("w4_kv_read", T, kv_heads, D, pages, page_size, cache_bits);
+    if (st != W4_OK) return st;
+    if (out_type != W4_F32 && out_type != W4_BF16) {
+        set_error("w4_kv_read: out_type is neither W4_F32 nor W4_BF16");
+        return W4_ERR_SHAPE;
+    }
+    if (T == 0) return W4_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache || (cache_bits == 8 && (!k_scale || !v_scale))) {
+        set_error("w4_kv_read: a required pointer is NULL");
+        return W4_ERR_NULL;
+    }
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        (cache_bits == 8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))) {
+        set_error("w4_kv_read: k, v and the caches must be 16-byte aligned, slots 8-byte, scales 4-byte");
+        return W4_ERR_ALIGN;
+    }
+    int dev = -1;
+    st = check_device(&dev);
+    if (st != W4_OK) return st;
+    KvParams p = {};
+    p.cache[0] = (void *)k_cache, p.cache[1] = (void *)v_cache;
+    p.scale[0] = (float *)k_scale, p.scale[1] = (float *)v_scale;
+    p.dst[0] = k, p.dst[1] = v, p.slots = slots;
+    p.T = T, p.pool = pages * page_size, p.heads = (int)kv_heads, p.page_size = (int)page_size;
+    const bool f32 = out_type == W4_F32;
+    if (D == 128)
+        cache_bits == 8 ? launch_read<128, true>(p, f32, (hipStream_t)stream)
+                        : launch_read<128, false>(p, f32, (hipStream_t)stream);
+    else
+        cache_bits == 8 ? launch_read<64, true>(p, f32, (hipStream_t)stream)
+                        : launch_read<64, false>(p, f32, (hipStream_t)stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("w4_kv_read launch", e);
+    return W4_OK;
+}
+
+}  // extern "C"

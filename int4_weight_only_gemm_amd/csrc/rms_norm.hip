@@ -1,0 +1,340 @@
+// rms_norm.hip -- residual addition and root-mean-square norm between two quantized linear
+// layers, with the output in the form the next product reads, for gfx950.
+//
+//     r   = T(residual + x)                    (T: the residual's type; r = x without one)
+//     inv = binary32(1 / sqrt(mean_h r^2 + eps))
+//     y   = (r * inv) * weight                 (two binary32 roundings)
+// and y as bfloat16 (the activations of w4a16_gemm and w8a16_gemm), as 4-bit codes with a
+// scale per group of 128 (the activations of w4a4_gemm, the codes that a4_quantize gives for
+// the bfloat16 y), or as 8-bit codes with a scale per group of 128.
+//
+// The sum of squares is taken in binary64: each square of a binary32 value is exact there, so
+// the order of the sum does not reach the binary32 result, and the codes are reproducible
+// bit for bit.  It costs one conversion and one fma a value, which a kernel bound by HBM hides.
+#include "internal.h"
+
+using namespace w4host;
+using namespace w4dev;
+
+namespace {
+
+constexpr int kGroup = 128;
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxChunks = 4;  // 8-value chunks a thread holds
+constexpr int64_t kMaxH = (int64_t)kMaxThreads * kMaxChunks * 8;
+
+struct NormParams {
+    const void *x, *res, *w;
+    void *y;
+    float *scales;
+    void *res_out;
+    double eps;
+    int64_t x_stride, res_stride;
+    int H;
+    int res_kind;  // 0 none, 1 float32, 2 bfloat16
+    int w_f32;
+    int bits;      // 16, 8, 4
+};
+
+// One workgroup per row, the row held in registers between the sum and the output, so every
+// input is read once.  A thread holds CH chunks of 8 consecutive values (chunk c of thread t
+// is number c * threads + t), so a group of 128 is one DPP row of 16 lanes.
+// VEC: 16-byte accesses; otherwise rows begin anywhere or end inside a chunk and every value
+// moves by itself.
+template <int CH, bool VEC, bool XF32>
+__global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(const NormParams p)
+{
+    __shared__ double s_sum[kMaxThreads / 64];
+    const int64_t row = blockIdx.x;
+    const int threads = blockDim.x, tid = threadIdx.x;
+    const int64_t xb = row * p.x_stride, rb = row * p.res_stride, ob = row * p.H;
+    float r[CH][8];
+    if constexpr (VEC) {
+        Raw8 xr[CH], rr[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * threads + tid) * 8;
+            if (e < p.H) xr[c] = load_raw8<XF32>(p.x, xb + e);
+        }
+        if (p.res_kind == 1) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * threads + tid) * 8;
+                if (e < p.H) rr[c] = load_raw8<true>(p.res, rb + e);
+            }
+        } else if (p.res_kind == 2) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int e = (c * threads + tid) * 8;
+                if (e < p.H) rr[c] = load_raw8<false>(p.res, rb + e);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e = (c * threads + tid) * 8;
+            if (e < p.H) {
+                raw8_to_float<XF32>(xr[c], r[c]);
+                float f[8];
+                if (p.res_kind == 1) {
+                    raw8_to_float<true>(rr[c], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) r[c][j] += f[j];
+                    float *dst = (float *)p.res_out + ob + e;
+                    *(f32x4 *)dst = f32x4{r[c][0], r[c][1], r[c][2], r[c][3]};
+                    *(f32x4 *)(dst + 4) = f32x4{r[c][4], r[c][5], r[c][6], r[c][7]};
+                } else if (p.res_kind == 2) {
+                    raw8_to_float<false>(rr[c], f);
+                    u32x4 v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = pack_bf16(r[c][2 * j] + f[2 * j], r[c][2 * j + 1] + f[2 * j + 1]);
+                        r[c][2 * j] = bf16_lo(v[j]);
+                        r[c][2 * j + 1] = bf16_hi(v[j]);
+                    }
+                    *(u32x4 *)((uint16_t *)p.res_out + ob + e) = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = (c * threads + tid) * 8 + j;
+                r[c][j] = 0.f;
+                if (e < p.H) {
+                    r[c][j] = load_one<XF32>(p.x, xb + e);
+                    if (p.res_kind == 1) {
+                        r[c][j] += load_one<true>(p.res, rb + e);
+                        ((float *)p.res_out)[ob + e] = r[c][j];
+                    } else if (p.res_kind == 2) {
+                        r[c][j] = round_bf16(r[c][j] + load_one<false>(p.res, rb + e));
+                        ((uint16_t *)p.res_out)[ob + e] = (uint16_t)(__builtin_bit_cast(uint32_t, r[c][j]) >> 16);
+                    }
+                }
+            }
+    }
+
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma((double)r[c][j], (double)r[c][j], sum);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+    __syncthreads();
+    sum = s_sum[0];
+    for (int i = 1; i < threads >> 6; ++i) sum += s_sum[i];
+    const float inv = (float)(1.0 / sqrt(sum / (double)p.H + p.eps));
+
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e = (c * threads + tid) * 8;
+        float y[8];
+        if (e < p.H) {
+            float w[8];
+            if constexpr (VEC) {
+                if (p.w_f32)
+                    raw8_to_float<true>(load_raw8<true>(p.w, e), w);
+                else
+                    raw8_to_float<false>(load_raw8<false>(p.w, e), w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[j] = 0.f;
+                    if (e + j < p.H) w[j] = p.w_f32 ? load_one<true>(p.w, e + j) : load_one<false>(p.w, e + j);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = (r[c][j] * inv) * w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = 0.f;
+        }
+        if (p.bits == 16) {
+            if constexpr (VEC) {
+                if (e < p.H) {
+                    const u32x4 v = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                                     pack_bf16(y[6], y[7])};
+                    *(u32x4 *)((uint16_t *)p.y + ob + e) = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (e + j < p.H) ((__bf16 *)p.y)[ob + e + j] = (__bf16)y[j];
+            }
+            continue;
+        }
+        // H is a multiple of 128 here: a DPP row holds a whole group or none of one
+        if (p.bits == 4) {
+            // through bfloat16, so that the codes are those of a4_quantize on the 16-bit output
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = round_bf16(y[j]);
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+        top = row16_fmax(top);
+        const float s = top / (p.bits == 4 ? 7.0f : 127.0f);
+        if (e < p.H) {
+            if (p.bits == 4) {
+                uint32_t word = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) word |= (uint32_t)(symmetric_code(y[j], s, -8.f, 7.f) + 8) << (4 * j);
+                ((uint32_t *)p.y)[(ob + e) >> 3] = word;
+            } else {
+                u32x2 word = {0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    word[j >> 2] |= (uint32_t)(symmetric_code(y[j], s, -127.f, 127.f) & 0xFF) << (8 * (j & 3));
+                *(u32x2 *)((uint8_t *)p.y + ob + e) = word;
+            }
+            if ((tid & 15) == 0) p.scales[(ob + e) / kGroup] = s;
+        }
+    }
+}
+
+// Codes and scales back to the values they stand for, 8 values a thread.
+__global__ __launch_bounds__(256) void act_dequantize_kernel(const void *__restrict__ codes,
+                                                             const float *__restrict__ scales,
+                                                             float *__restrict__ out, int64_t chunks, int bits)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
+        const float s = scales[i >> 4];
+        float v[8];
+        if (bits == 4) {
+            const uint32_t w = ((const uint32_t *)codes)[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (float)((int)((w >> (4 * j)) & 0xFu) - 8) * s;
+        } else {
+            const u32x2 w = ((const u32x2 *)codes)[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)(w[j >> 2] >> (8 * (j & 3))) * s;
+        }
+        f32x4 *dst = (f32x4 *)(out + i * 8);
+        dst[0] = f32x4{v[0], v[1], v[2], v[3]};
+        dst[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+}
+
+template <int CH>
+void launch_norm(const NormParams &p, bool vec, bool x_f32, int64_t M, int threads, hipStream_t stream)
+{
+    const dim3 grid((unsigned)M), block((unsigned)threads);
+    if (vec && x_f32)
+        hipLaunchKernelGGL((rms_norm_kernel<CH, true, true>), grid, block, 0, stream, p);
+    else if (vec)
+        hipLaunchKernelGGL((rms_norm_kernel<CH, true, false>), grid, block, 0, stream, p);
+    else if (x_f32)
+        hipLaunchKernelGGL((rms_norm_kernel<CH, false, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((rms_norm_kernel<CH, false, false>), grid, block, 0, stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+w4_status w4_rms_norm(const void *x, int x_type, int64_t x_stride, const void *residual, int residual_type,
+                      int64_t residual_stride, const void *weight, int weight_type, double eps, void *y, int y_bits,
+                      float *y_scales, void *residual_out, int64_t M, int64_t H, void *stream)
+{
+    if ((x_type != W4_F32 && x_type != W4_BF16) || (weight_type != W4_F32 && weight_type != W4_BF16) ||
+        (residual && residual_type != W4_F32 && residual_type != W4_BF16)) {
+        set_error("w4_rms_norm: a type is neither W4_F32 nor W4_BF16");
+        return W4_ERR_SHAPE;
+    }
+    if (y_bits != 16 && y_bits != 8 && y_bits != 4) {
+        set_error("w4_rms_norm: y_bits=%d: need 16, 8 or 4", y_bits);
+        return W4_ERR_SHAPE;
+    }
+    if (M < 0 || M > 0x7FFFFFFF || H < 1 || H > kMaxH || (y_bits != 16 && H % kGroup != 0) ||
+        M > ((int64_t)1 << 40) / H) {
+        set_error("w4_rms_norm: shape M=%lld H=%lld: need M>=0, 1<=H<=%lld, H%%128==0 for 8- and 4-bit output",
+                  (long long)M, (long long)H, (long long)kMaxH);
+        return W4_ERR_SHAPE;
+    }
+    const int64_t lim = (int64_t)1 << 40;
+    if (x_stride < H || x_stride > lim || (residual && (residual_stride < H || residual_stride > lim))) {
+        set_error("w4_rms_norm: a row stride is below H=%lld or too large", (long long)H);
+        return W4_ERR_SHAPE;
+    }
+    if (!(eps >= 0.0)) {
+        set_error("w4_rms_norm: eps must be at least 0");
+        return W4_ERR_SHAPE;
+    }
+    if (M == 0) return W4_OK;
+    if (!x || !weight || !y || (residual && !residual_out) || (y_bits != 16 && !y_scales)) {
+        set_error("w4_rms_norm: a required pointer is NULL");
+        return W4_ERR_NULL;
+    }
+    const int xs = x_type == W4_F32 ? 4 : 2, ws = weight_type == W4_F32 ? 4 : 2;
+    const int rs = residual_type == W4_F32 ? 4 : 2;
+    if (!aligned(x, xs) || !aligned(weight, ws) || (residual && (!aligned(residual, rs) || !aligned(residual_out, rs))) ||
+        !aligned(y, y_bits == 16 ? 2 : y_bits == 8 ? 8 : 4) || (y_bits != 16 && !aligned(y_scales, 4))) {
+        set_error("w4_rms_norm: a pointer is not aligned to its type (8-bit codes: 8 bytes, 4-bit codes: 4 bytes)");
+        return W4_ERR_ALIGN;
+    }
+    int dev = -1;
+    w4_status st = check_device(&dev);
+    if (st != W4_OK) return st;
+    bool vec = H % 8 == 0 && aligned(x, 16) && x_stride * xs % 16 == 0 && aligned(weight, 16) &&
+               (y_bits != 16 || aligned(y, 16));
+    if (residual)
+        vec = vec && aligned(residual, 16) && residual_stride * rs % 16 == 0 && aligned(residual_out, 16);
+    NormParams p;
+    p.x = x, p.res = residual, p.w = weight, p.y = y, p.scales = y_scales, p.res_out = residual_out;
+    p.eps = eps, p.x_stride = x_stride, p.res_stride = residual_stride, p.H = (int)H;
+    p.res_kind = !residual ? 0 : residual_type == W4_F32 ? 1 : 2;
+    p.w_f32 = weight_type == W4_F32, p.bits = y_bits;
+    const int chunks = (int)((H + 7) / 8);
+    const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
+    const int threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
+    if (ch == 1)
+        launch_norm<1>(p, vec, x_type == W4_F32, M, threads, (hipStream_t)stream);
+    else if (ch == 2)
+        launch_norm<2>(p, vec, x_type == W4_F32, M, threads, (hipStream_t)stream);
+    else
+        launch_norm<4>(p, vec, x_type == W4_F32, M, threads, (hipStream_t)stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("w4_rms_norm launch", e);
+    return W4_OK;
+}
+
+w4_status w4_act_dequantize(const void *codes, const float *scales, float *out, int64_t M, int64_t K, int bits,
+                            void *stream)
+{
+    if (bits != 8 && bits != 4) {
+        set_error("w4_act_dequantize: bits=%d: need 8 or 4", bits);
+        return W4_ERR_SHAPE;
+    }
+    if (M < 0 || K < kGroup || K % kGroup != 0 || M > ((int64_t)1 << 40) / K) {
+        set_error("w4_act_dequantize: shape M=%lld K=%lld: need M>=0, K>=128, K%%128==0", (long long)M, (long long)K);
+        return W4_ERR_SHAPE;
+    }
+    if (M == 0) return W4_OK;
+    if (!codes || !scales || !out) {
+        set_error("w4_act_dequantize: a required pointer is NULL");
+        return W4_ERR_NULL;
+    }
+    if (!aligned(codes, bits == 8 ? 8 : 4) || !aligned(scales, 4) || !aligned(out, 16)) {
+        set_error("w4_act_dequantize: codes must be aligned to 8 values, scales to 4 bytes and out to 16");
+        return W4_ERR_ALIGN;
+    }
+    int dev = -1;
+    w4_status st = check_device(&dev);
+    if (st != W4_OK) return st;
+    const int64_t chunks = M * (K / 8);
+    const int64_t blocks = (chunks + 255) / 256;
+    hipLaunchKernelGGL(act_dequantize_kernel, dim3((unsigned)(blocks > 65536 ? 65536 : blocks)), dim3(256), 0,
+                       (hipStream_t)stream, codes, scales, out, chunks, bits);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("w4_act_dequantize launch", e);
+    return W4_OK;
+}
+
+}  // extern "C"

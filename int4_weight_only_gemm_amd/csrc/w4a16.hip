@@ -47,7 +47,10 @@
 #include <utility>
 #include <vector>
 
+#include "internal.h"
 #include "w4a16.h"
+
+using namespace w4host;
 
 namespace {
 
@@ -1747,7 +1750,13 @@ __global__ __launch_bounds__(256) void w4_read_probe_kernel(const void *src, uin
 // ------------------------------------------------------------------------------------
 // Host side
 
-thread_local std::string g_last_error;
+// Error text, device check and workspaces, shared with the other sources of the library
+// (declared in internal.h).
+}  // namespace
+
+namespace w4host {
+
+static thread_local std::string g_last_error;
 
 void set_error(const char *fmt, ...)
 {
@@ -1767,8 +1776,8 @@ w4_status hip_fail(const char *what, hipError_t e)
     return W4_ERR_HIP;
 }
 
-std::mutex g_mutex;
-std::map<int, int> g_device_ok;  // device -> 1 gfx950, 0 other
+static std::mutex g_mutex;
+static std::map<int, int> g_device_ok;  // device -> 1 gfx950, 0 other
 
 w4_status check_device(int *dev_out)
 {
@@ -1804,8 +1813,8 @@ struct Workspace {
     size_t counters = 0;     // capacity of the counter region, in counters
     size_t part_bytes = 0;   // capacity of the partial region
 };
-std::map<std::pair<int, hipStream_t>, Workspace> g_workspaces;
-std::vector<char *> g_retired;  // superseded buffers stay valid for graphs captured earlier
+static std::map<std::pair<int, hipStream_t>, Workspace> g_workspaces;
+static std::vector<char *> g_retired;  // superseded buffers stay valid for graphs captured earlier
 
 // Workspace layout, fixed for the life of a buffer: [counters][partials], the partial
 // region starting at counters * 4 rounded up to 256 bytes.  Counters are zero whenever no
@@ -1845,6 +1854,10 @@ w4_status get_workspace(int dev, hipStream_t stream, size_t tiles, size_t part_b
     *part = (float *)(ws.ptr + ws.counters * 4);
     return W4_OK;
 }
+
+}  // namespace w4host
+
+namespace {
 
 // Scratch for the entry point that allocates nothing (w4a16_gemm_noalloc): a file-scope
 // device array with the workspace's layout, [arrival counters][partials], fixed for the life

@@ -1,0 +1,141 @@
+"""The paged key/value cache: what is written, bit for bit, what is left alone, what is read back."""
+import pytest
+import torch
+
+import int4_weight_only_gemm_amd as w4
+from gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def expected(x, bits):
+    """Codes (or bfloat16 values) and scales of [T, heads, D], by binary32 steps on the host."""
+    x = x.float()
+    if bits == 16:
+        return x.to(BF16), None
+    s = x.abs().amax(-1) / torch.tensor(127.0)
+    q = torch.where(s[..., None] > 0, (x / s[..., None]).round().clamp(-127, 127), torch.zeros(()))
+    return q.to(torch.int8), s
+
+
+def pools(pages, heads, page, D, bits, g):
+    shape = (pages, heads, page, D)
+    if bits == 16:
+        return [torch.randn(shape, generator=g).to(BF16) for _ in range(2)] + [None, None]
+    return ([torch.randint(-127, 128, shape, generator=g, dtype=torch.int8) for _ in range(2)]
+            + [torch.rand(shape[:3], generator=g) for _ in range(2)])
+
+
+CASES = [(1, 1, 64, 1, 3), (5, 4, 128, 64, 4), (17, 2, 128, 16, 9), (100, 3, 64, 48, 5), (257, 32, 128, 16, 20),
+         (40, 8, 64, 7, 11), (1000, 1, 128, 256, 6)]
+
+
+@pytest.mark.parametrize("T,heads,D,page,pages", CASES)
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("src", [F32, BF16])
+def test_write_and_read(T, heads, D, page, pages, bits, src):
+    g = torch.Generator().manual_seed(T + heads + D + page + bits)
+    log(f"kv T={T} heads={heads} D={D} page={page} pages={pages} bits={bits} {src}")
+    kc, vc, ks, vs = pools(pages, heads, page, D, bits, g)
+    k = torch.randn(T, heads, D, generator=g).to(src)
+    v = (torch.randn(T, heads, D, generator=g) * 10 ** (3 * torch.rand(T, heads, 1, generator=g) - 1)).to(src)
+    k[0, 0] = 0                                           # an empty grid
+    slots = torch.randperm(pages * page, generator=g)[:T].clone()
+    T = len(slots)                                        # some pools are smaller than T
+    k, v = k[:T], v[:T]
+    if T > 4:
+        slots[2], slots[3] = -1, pages * page             # padding: skipped
+    dev = [x if x is None else x.cuda() for x in (kc, vc, ks, vs)]
+    w4.kv_write(k.cuda(), v.cuda(), slots.cuda(), *dev)
+    live = (slots >= 0) & (slots < pages * page)
+    at, off = slots[live] // page, slots[live] % page
+    for x, cache, scale in ((k, kc, ks), (v, vc, vs)):
+        q, s = expected(x, bits)
+        cache[at, :, off] = q[live]
+        if scale is not None:
+            scale[at, :, off] = s[live]
+    for got, want in zip(dev, (kc, vc, ks, vs)):          # the rest of the pool is untouched
+        assert got is None or torch.equal(got.cpu(), want)
+    for kind in (F32, BF16):
+        for got, cache, scale in zip(w4.kv_read(slots.cuda(), *dev, dtype=kind), (kc, vc), (ks, vs)):
+            want = torch.zeros(T, heads, D)
+            want[live] = cache[at, :, off].float() * (1 if scale is None else scale[at, :, off][..., None])
+            assert got.dtype == kind and torch.equal(got.cpu(), want.to(kind))
+
+
+@pytest.mark.parametrize("src", [F32, BF16])
+def test_strides_and_alignment(src):
+    # slices of a fused qkv row; a row that begins off the vector path's alignment; heads swapped
+    # with tokens; one row for all tokens (stride 0)
+    T, heads, D, page = 21, 4, 128, 16
+    g = torch.Generator().manual_seed(7)
+    wide = torch.randn(T, 3 * heads * D + 9, generator=g).to(src).cuda()
+    for off in (0, 1, 8):
+        qkv = wide[:, off:off + 3 * heads * D].unflatten(1, (3 * heads, D))
+        for k, v in ((qkv[:, heads:2 * heads], qkv[:, 2 * heads:]),
+                     (qkv[:heads, :T].transpose(0, 1)[:8], qkv[1:heads + 1, :T].transpose(0, 1)[:8]),
+                     (qkv[:1, :heads].expand(T, heads, D), qkv[:, :heads])):
+            log(f"kv strides {src} offset={off} {tuple(k.stride())}")
+            slots = torch.randperm(64, generator=g)[:k.shape[0]].cuda()
+            a = [torch.zeros(4, heads, page, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+            a += [torch.zeros(4, heads, page, device="cuda") for _ in range(2)]
+            b = [x.clone() for x in a]
+            w4.kv_write(k, v, slots, *a)
+            w4.kv_write(k.contiguous(), v.contiguous(), slots, *b)
+            q, s = expected(k.cpu(), 8)
+            assert torch.equal(a[0].cpu()[slots.cpu() // page, :, slots.cpu() % page], q)
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
+def test_slots_past_32_bits():
+    # a pool of more than 2^31 values: the last page lies past 32-bit element and byte offsets
+    heads, page, D = 32, 64, 128
+    pages = (1 << 32) // (heads * page * D) + 3
+    kc = torch.zeros(pages, heads, page, D, dtype=torch.int8, device="cuda")
+    vc = torch.zeros_like(kc)
+    ks = torch.zeros(pages, heads, page, device="cuda")
+    vs = torch.zeros_like(ks)
+    g = torch.Generator().manual_seed(9)
+    k, v = torch.randn(3, heads, D, generator=g), torch.randn(3, heads, D, generator=g)
+    slots = torch.tensor([0, pages * page - 1, pages * page // 2])
+    log("kv slots past 32 bits")
+    w4.kv_write(k.cuda(), v.cuda(), slots.cuda(), kc, vc, ks, vs)
+    for x, cache, scale in ((k, kc, ks), (v, vc, vs)):
+        q, s = expected(x, 8)
+        for t in range(3):
+            p, o = int(slots[t]) // page, int(slots[t]) % page
+            assert torch.equal(cache[p, :, o].cpu(), q[t]) and torch.equal(scale[p, :, o].cpu(), s[t])
+    k2, v2 = w4.kv_read(slots.cuda(), kc, vc, ks, vs, dtype=F32)
+    q, s = expected(v, 8)
+    assert torch.equal(v2.cpu(), q.float() * s[..., None])
+    assert int(kc.ne(0).any(-1).any(1).sum()) == 3        # three tokens, and no other place
+
+
+def test_empty_streams_and_refusals():
+    c = [torch.zeros(2, 2, 16, 64, dtype=torch.int8, device="cuda") for _ in range(2)]
+    s = [torch.zeros(2, 2, 16, device="cuda") for _ in range(2)]
+    k = torch.randn(3, 2, 64, device="cuda")
+    slots = torch.tensor([0, 5, 31], device="cuda")
+    w4.kv_write(k[:0], k[:0], slots[:0], *c, *s)
+    assert w4.kv_read(slots[:0], *c, *s)[0].shape == (0, 2, 64)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    w4.kv_write(k, k, slots, *c, *s, stream=other)
+    got = w4.kv_read(slots, *c, *s, dtype=F32, stream=other)
+    other.synchronize()
+    q, sc = expected(k.cpu(), 8)
+    assert torch.equal(got[1].cpu(), q.float() * sc[..., None])
+    bad = [dict(k_scale=None), dict(v_cache=c[1].view(2, 16, 2, 64)), dict(v=k[:2]), dict(v=k.to(BF16)),
+           dict(slots=slots[:2]), dict(slots=slots.int()), dict(k=k.cpu()), dict(k=k.half()),
+           dict(k_scale=s[0].view(2, 16, 2)), dict(k_cache=c[0].float()), dict(k=k.transpose(1, 2))]
+    for change in bad:
+        args = dict(k=k, v=k, slots=slots, k_cache=c[0], v_cache=c[1], k_scale=s[0], v_scale=s[1])
+        args.update(change)
+        with pytest.raises((ValueError, TypeError)):
+            w4.kv_write(**args)
+    with pytest.raises(TypeError):
+        w4.kv_read(slots, *c, *s, dtype=torch.float16)
+    with pytest.raises(w4.W4Error):
+        w4.kv_read(slots, *[torch.zeros(2, 2, 16, 96, dtype=BF16, device="cuda")] * 2)

@@ -1,0 +1,298 @@
+"""Attention over the paged cache against a plain implementation in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import int4_weight_only_gemm_amd as w4
+from gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+class Case:
+    """A batch over a shuffled pool whose unused places hold NaN (16 bits) or wild scales (8 bits)."""
+
+    def __init__(self, ns, kvs, hq, hkv, D, page, bits, seed=0, spare=3, width_pad=2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.ns, self.kvs, self.hq, self.hkv, self.D, self.page, self.bits = ns, kvs, hq, hkv, D, page, bits
+        B, T = len(ns), sum(ns)
+        used = [-(-kv // page) for kv in kvs]
+        pages = sum(used) + spare
+        order = torch.randperm(pages, generator=g, device="cuda").tolist()
+        width = max(used + [0]) + width_pad
+        table = torch.full((B, width), -7, dtype=torch.int32)      # never read past a sequence's pages
+        shape = (pages, hkv, page, D)
+        if bits == 16:
+            kc, vc = (torch.full(shape, float("nan"), dtype=BF16, device="cuda") for _ in range(2))
+            ks = vs = None
+        else:
+            kc, vc = (torch.randint(-128, 128, shape, dtype=torch.int8, device="cuda", generator=g) for _ in range(2))
+            ks, vs = (torch.full(shape[:3], float("nan"), device="cuda") for _ in range(2))
+        self.k, self.v = [], []                                    # per sequence [kv, hkv, D], 64 bits
+        at = 0
+        for b, kv in enumerate(kvs):
+            table[b, :used[b]] = torch.tensor(order[at:at + used[b]], dtype=torch.int32)
+            at += used[b]
+            slots = torch.tensor([int(table[b, j // page]) * page + j % page for j in range(kv)], dtype=torch.int64,
+                                 device="cuda")
+            k, v = rnd(kv, hkv, D), rnd(kv, hkv, D)
+            if kv:
+                w4.kv_write(k, v, slots, kc, vc, ks, vs)
+                k, v = w4.kv_read(slots, kc, vc, ks, vs, dtype=F32)
+            self.k.append(k.double())
+            self.v.append(v.double())
+        self.q = (1.5 * rnd(T, hq, D)).to(BF16)
+        self.table = table.cuda()
+        self.q_start = torch.tensor([sum(ns[:b]) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+        self.kv_len = torch.tensor(kvs, dtype=torch.int32, device="cuda")
+        self.cache = (kc, vc, ks, vs)
+
+    def run(self, **kw):
+        kc, vc, ks, vs = self.cache
+        args = dict(q=self.q, k_cache=kc, v_cache=vc, block_table=self.table, q_start=self.q_start, kv_len=self.kv_len,
+                    max_q=max(self.ns), max_kv=max(self.kvs), k_scale=ks, v_scale=vs)
+        args.update(kw)
+        return w4.paged_attention(**args)
+
+    def exact(self, scale=None):
+        """Outputs and bounds. The bound: half a bfloat16 step of the output; half a step of each
+        weight (bfloat16) against sum_j p_j |v_j|; and in binary32, each rounding taken twice as large
+        as nearest: D products of a score, kv terms of a sum, a few steps of a weight."""
+        scale = self.D ** -0.5 if scale is None else scale
+        G = self.hq // self.hkv
+        out, bound, at = torch.zeros(self.q.shape, dtype=torch.float64, device="cuda"), None, 0
+        bound = torch.zeros_like(out)
+        for b, (n, kv) in enumerate(zip(self.ns, self.kvs)):
+            pos = torch.arange(n, device="cuda") + kv - n
+            sees = torch.arange(kv, device="cuda")[None] <= pos[:, None]
+            some = sees.any(1)
+            for h in range(self.hq):
+                if not kv or not n:
+                    continue
+                q = self.q[at:at + n, h].double()
+                k, v = self.k[b][:, h // G].contiguous(), self.v[b][:, h // G].contiguous()
+                s = (q @ k.t().contiguous() * scale).masked_fill(~sees, -math.inf)
+                p = torch.softmax(s, 1)
+                p = torch.where(some[:, None], p, torch.zeros_like(p))
+                o, a = p @ v, p @ v.abs()
+                top = (q.abs() @ k.abs().t().contiguous() * abs(scale)).masked_fill(~sees, 0).amax(1, keepdim=True)
+                rel = 2.0 ** -8 + 2 * (2.0 ** -23 * (self.D * top + kv + 8))
+                out[at:at + n, h] = o
+                bound[at:at + n, h] = o.abs() * 2.0 ** -8 + a * rel + 1e-30
+            at += n
+        return out, bound
+
+    def check(self, got, what, scale=None, rows=None):
+        out, bound = self.exact(scale)
+        got = got.double()
+        if rows is not None:
+            got, out, bound = got[rows], out[rows], bound[rows]
+        assert torch.isfinite(got).all(), f"{what}: {int((~torch.isfinite(got)).sum())} values are not finite"
+        bad = (got - out).abs() > bound
+        if bad.any():
+            i = bad.nonzero()[0].tolist()
+            raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} out of bounds; first {i}: "
+                                 f"{got[tuple(i)].item()} not {out[tuple(i)].item()} +- {bound[tuple(i)].item()}")
+
+
+SHAPES = [  # new tokens, cached tokens, per sequence
+    ([1], [1]), ([1], [2]), ([1], [15]), ([1], [16]), ([1], [17]), ([1], [777]), ([5], [5]), ([5], [33]), ([3], [4097]),
+    ([1, 5, 2, 1], [31, 32, 33, 900]), ([2, 0, 4], [64, 50, 300]), ([9], [130]), ([70], [70]), ([33], [1000]),
+    ([200, 7], [333, 65]), ([64, 128, 300], [64, 1000, 301])]
+HEADS = [(12, 2, 128), (28, 4, 128), (4, 4, 64), (8, 1, 64)]
+
+
+@pytest.mark.parametrize("ns,kvs", SHAPES, ids=lambda x: "-".join(map(str, x)))
+@pytest.mark.parametrize("hq,hkv,D", HEADS)
+@pytest.mark.parametrize("page,bits", [(16, 16), (64, 8), (48, 8), (128, 16)])
+def test_chunks(ns, kvs, hq, hkv, D, page, bits):
+    what = f"attention n={ns} kv={kvs} heads={hq}/{hkv} D={D} page={page} bits={bits}"
+    log(what)
+    c = Case(ns, kvs, hq, hkv, D, page, bits, seed=len(ns) + kvs[0])
+    got = c.run()
+    c.check(got, what)
+    assert torch.equal(got, c.run()), f"{what}: two runs differ"
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_empty_rows_and_sequences(bits, D):
+    # more new tokens than cached ones: the first rows see nothing; a sequence without any token
+    c = Case([6, 3, 2, 40], [2, 0, 2, 17], 8, 2, D, 16, bits, seed=3)
+    log(f"attention empty rows bits={bits} D={D}")
+    got = c.run()
+    assert (got[:4] == 0).all() and (got[6:9] == 0).all() and (got[11:34] == 0).all()
+    c.check(got, "empty rows")
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_many_sequences_and_long_ones(bits):
+    ns = [1 + b % 6 for b in range(40)]
+    kvs = [7 + 61 * b % 1500 for b in range(40)]
+    c = Case(ns, [max(n, kv) for n, kv in zip(ns, kvs)], 8, 4, 128, 64, bits, seed=5)
+    log(f"attention 40 sequences bits={bits}")
+    c.check(c.run(), "40 sequences")
+    c = Case([2, 1], [40003, 12], 8, 1, 128, 256, bits, seed=6)
+    log(f"attention 40003 tokens bits={bits}")
+    c.check(c.run(), "40003 tokens")
+    log(f"attention chunk of 500 over 9000 bits={bits}")
+    c = Case([500], [9000], 8, 2, 128, 64, bits, seed=8)
+    c.check(c.run(), "500 over 9000")
+
+
+@pytest.mark.parametrize("n", [1, 5, 150])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_group_sizes(n, bits):
+    for hq, hkv in ((1, 1), (3, 1), (5, 5), (17, 1), (64, 1), (6, 3)):
+        c = Case([n, 1], [n + 90, 50], hq, hkv, 64, 16, bits, seed=hq)
+        log(f"attention heads {hq}/{hkv} n={n} bits={bits}")
+        c.check(c.run(), f"heads {hq}/{hkv}")
+
+
+@pytest.mark.parametrize("n", [4, 100])
+def test_strides_scale_and_out(n):
+    c = Case([n, 3], [n + 200, 77], 6, 2, 128, 32, 8, seed=9)
+    T = sum(c.ns)
+    want = c.run()
+    for off in (0, 8, 1):                                    # slices of a fused row; off 1: unaligned rows
+        wide = torch.randn(T, 10 * 128 + 16, device="cuda").to(BF16)
+        view = wide[:, off:off + 10 * 128].unflatten(1, (10, 128))[:, 2:8]
+        view.copy_(c.q)
+        log(f"attention strided q offset={off} n={n}")
+        assert torch.equal(c.run(q=view), want)
+    heads_first = c.q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(c.run(q=heads_first), want)
+    wide_table = torch.full((2, c.table.shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+    wide_table[:, :c.table.shape[1]] = c.table
+    assert torch.equal(c.run(block_table=wide_table[:, :c.table.shape[1]]), want)
+    out = torch.full_like(c.q, 7.0)
+    assert c.run(out=out) is out and torch.equal(out, want)
+    c.check(c.run(max_kv=1), "low hint")
+    c.check(c.run(max_kv=100000), "high hint")
+    c.check(c.run(scale=0.5), "scale 0.5", scale=0.5)
+    c.check(c.run(scale=-0.2), "negative scale", scale=-0.2)
+
+
+@pytest.mark.parametrize("n", [2, 80])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_bad_pages_give_nan_where_they_are_seen(n, bits):
+    c = Case([n, 2, 2], [n + 60, 40, 90], 4, 2, 64, 16, bits, seed=12)
+    good = c.run()
+    table = c.table.clone()
+    table[0, (n + 60 - 1) // 16] = c.cache[0].shape[0]       # the last page of sequence 0: seen by its last rows
+    table[1, 0] = -1                                         # the first page of sequence 1: seen by all
+    log(f"attention bad pages n={n} bits={bits}")
+    got = c.run(block_table=table)
+    first_seeing = (n + 60 - 1) // 16 * 16 - 60              # row whose position enters that page
+    first_seeing = max(0, first_seeing)
+    assert torch.isnan(got[first_seeing:n + 2]).all()
+    assert torch.equal(got[:first_seeing], good[:first_seeing]) and torch.equal(got[n + 2:], good[n + 2:])
+    narrow = c.run(block_table=c.table[:, :3].contiguous())  # 48 tokens of room
+    rows = max(0, 48 - 60)
+    assert torch.isnan(narrow[rows:n]).all() and torch.equal(narrow[n:n + 2], good[n:n + 2])
+    assert torch.isnan(narrow[n + 2:]).all()
+    none = c.run(block_table=torch.zeros(3, 0, dtype=torch.int32, device="cuda"))
+    assert torch.isnan(none).all()
+
+
+@pytest.mark.parametrize("n", [3, 130])
+def test_bad_offsets_stay_inside(n):
+    # offsets out of order or past the rows are cut to what lies inside; other rows keep their values
+    c = Case([n, 4], [n + 50, 60], 4, 2, 64, 16, 16, seed=14)
+    good = c.run()
+    out = torch.full_like(c.q, 5.0)
+    bad = torch.tensor([0, n, n + 4000], dtype=torch.int32, device="cuda")
+    log(f"attention bad offsets n={n}")
+    assert torch.equal(c.run(q_start=bad, out=out), good)
+    out.fill_(5.0)
+    back = torch.tensor([0, n, n - 2], dtype=torch.int32, device="cuda")
+    c.run(q_start=back, out=out)
+    assert torch.equal(out[:n], good[:n]) and (out[n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("n,kv", [(1, 700), (5, 700), (90, 700)])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_large_scores(n, kv, bits):
+    # scores of several hundred, and one key that takes all the weight, late and early
+    c = Case([n], [kv], 4, 1, 128, 16, bits, seed=15)
+    c.q.mul_(20)
+    log(f"attention large scores n={n} bits={bits}")
+    c.check(c.run(), "large scores")
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("n", [6, 90])
+def test_what_a_row_does_not_see_may_be_anything(bits, n):
+    # infinities and NaN at the chunk's later tokens reach no row before them
+    c = Case([n], [n + 41], 4, 2, 64, 16, bits, seed=16)
+    good = c.run()
+    kc, vc, ks, vs = c.cache
+    for value in (float("nan"), float("inf"), -float("inf"), torch.finfo(BF16).max):
+        for i in (n - 1, n // 2):
+            j = 41 + i                                       # the token of row i
+            page, off = int(c.table[0, j // 16]), j % 16
+            for cache, scale in ((kc, ks), (vc, vs)):
+                kept = cache[page, :, off].clone() if bits == 16 else scale[page, :, off].clone()
+                if bits == 16:
+                    cache[page, :, off, ::3] = value
+                else:
+                    scale[page, :, off] = value
+                log(f"attention unseen {value} bits={bits} n={n} row={i}")
+                got = c.run()
+                if bits == 16:
+                    cache[page, :, off] = kept
+                else:
+                    scale[page, :, off] = kept
+                assert torch.equal(got[:i], good[:i])
+                if value != value:
+                    assert torch.isnan(got[i:]).any(-1).all()   # those that see it
+
+
+def test_streams_graph_and_refusals():
+    c = Case([5, 5], [900, 800], 28, 4, 128, 64, 8, seed=17)
+    want = c.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    q, lens = c.q.clone(), c.kv_len.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        assert torch.equal(c.run(q=q), want)                 # sizes the stream's workspace
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = c.run(q=q, kv_len=lens)
+        for i in range(5):
+            q.copy_(torch.randn(q.shape, device="cuda"))
+            lens.copy_(torch.tensor([900 - 37 * i, 800 - 111 * i]))
+            graph.replay()
+            s.synchronize()
+            again = got.clone()
+            eager = c.run(q=q, kv_len=lens)
+            s.synchronize()
+            assert torch.equal(again, eager), f"replay {i}"
+    kc, vc, ks, vs = c.cache
+    assert c.run(q=c.q[:0], max_q=0).shape == (0, 28, 128)
+    for change in (dict(q=c.q.float()), dict(q=c.q[:, :27]), dict(q=c.q[:, :, :64]), dict(block_table=c.table.long()),
+                   dict(block_table=c.table.t()), dict(q_start=c.q_start[:2]), dict(kv_len=c.kv_len.long()),
+                   dict(kv_len=c.kv_len[:1]), dict(k_scale=None), dict(out=torch.empty_like(c.q[:3])), dict(q=c.q.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            c.run(**change)
+    with pytest.raises(w4.W4Error):
+        c.run(max_q=11)
+
+
+def test_pool_past_32_bits():
+    # pages whose first value lies past 2^31 and 2^32
+    hkv, page, D = 8, 64, 128
+    pages = (1 << 32) // (hkv * page * D) + 4
+    kc = torch.zeros(pages, hkv, page, D, dtype=BF16, device="cuda")
+    vc = torch.zeros_like(kc)
+    c = Case([5], [300], 16, hkv, D, page, 16, seed=18)
+    want = c.run()
+    at = torch.tensor([pages - 1, 3, pages - 2, pages // 2 + 1, 7], dtype=torch.int32, device="cuda")
+    kc[at.long()], vc[at.long()] = c.cache[0][c.table[0, :5].long()], c.cache[1][c.table[0, :5].long()]
+    log("attention pool past 32 bits")
+    assert torch.equal(c.run(k_cache=kc, v_cache=vc, block_table=at[None].contiguous()), want)

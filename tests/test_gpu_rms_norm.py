@@ -1,0 +1,145 @@
+"""Residual + RMS norm against the definition in 64 bits, its codes bit for bit against binary32
+steps on the host."""
+import pytest
+import torch
+
+import int4_weight_only_gemm_amd as w4
+from gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}   # half a step, relative
+
+
+def inputs(M, H, x_type, res_type, w_type, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, H, generator=g).to(x_type)
+    res = None if res_type is None else (3 * torch.randn(M, H, generator=g)).to(res_type)
+    w = (1 + 0.3 * torch.randn(H, generator=g)).to(w_type)
+    return x, res, w
+
+
+def steps(x, res, w, eps):
+    """r and the binary32 y by the definition's steps, on the host."""
+    r = x if res is None else (x.float() + res.float()).to(res.dtype)
+    f = r.float()
+    inv = (1.0 / (f.double().square().mean(1, keepdim=True) + eps).sqrt()).float()
+    return r, (f * inv) * w.float()
+
+
+def codes_of(y, most, least):
+    g = y.view(y.shape[0], -1, 128)
+    s = g.abs().amax(-1) / torch.tensor(float(most))
+    q = torch.where(s[..., None] > 0, (g / s[..., None]).round().clamp(least, most), torch.zeros(()))
+    return q.view(y.shape).to(torch.int32), s
+
+
+SHAPES = [(1, 1), (1, 7), (3, 128), (2, 1000), (5, 1536), (7, 2049), (33, 3584), (4, 4096), (3, 8192), (2, 18944),
+          (1, 32768), (300, 136)]
+
+
+@pytest.mark.parametrize("M,H", SHAPES)
+@pytest.mark.parametrize("x_type,res_type,w_type", [(F32, BF16, BF16), (BF16, None, F32), (F32, F32, F32),
+                                                    (BF16, BF16, BF16), (F32, None, BF16), (BF16, F32, BF16)])
+def test_bf16_output(M, H, x_type, res_type, w_type):
+    x, res, w = inputs(M, H, x_type, res_type, w_type, M + H)
+    log(f"rms_norm M={M} H={H} {x_type} {res_type} {w_type}")
+    got = w4.rms_norm(x.cuda(), w.cuda(), None if res is None else res.cuda(), eps=1e-5)
+    y, r = (got, x) if res is None else (got[0].cpu(), got[1].cpu())
+    y = y.cpu()
+    assert y.dtype == BF16
+    if res is not None:
+        want = (x.float() + res.float()).to(res_type)   # one binary32 sum, one rounding: exact steps
+        assert r.dtype == res_type and torch.equal(r, want)
+    rd = r.double()
+    exact = rd / (rd.square().mean(1, keepdim=True) + 1e-5).sqrt() * w.double()
+    # three binary32 roundings (inv and two products), then half a step of bfloat16
+    bound = exact.abs() * ((1 + 2.0 ** -24) ** 3 * (1 + HALF[BF16]) - 1) + 1e-38
+    assert ((y.double() - exact).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M,H", [(1, 128), (5, 1536), (32, 4096), (3, 3584), (130, 256), (2, 32768)])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("x_type,res_type", [(F32, BF16), (BF16, None), (BF16, F32)])
+def test_codes_bit_for_bit(M, H, bits, x_type, res_type):
+    x, res, w = inputs(M, H, x_type, res_type, BF16, 3 * M + H + bits)
+    x[0, :128] = 0
+    if res is not None:
+        res[0, :128] = 0                                  # a group of zeros
+    log(f"rms_norm codes M={M} H={H} bits={bits} {x_type} {res_type}")
+    got = w4.rms_norm(x.cuda(), w.cuda(), None if res is None else res.cuda(), bits=bits)
+    r, y = steps(x, res, w, 1e-6)
+    if res is not None:
+        assert torch.equal(got[2].cpu(), r)
+    values = w4.dequantize_activations(got[0], got[1], bits=bits).cpu()
+    if bits == 8:
+        q, s = codes_of(y, 127, -127)
+        assert torch.equal(got[0].cpu().to(torch.int32), q)
+    else:
+        q, s = codes_of(y.to(BF16).float(), 7, -8)
+        b = got[0].cpu()
+        nib = torch.stack([(b >> (4 * j)) & 15 for j in range(8)], -1).view(M, H) - 8
+        assert torch.equal(nib, q)
+        # the same as the activation quantizer on the 16-bit output
+        y16 = w4.rms_norm(x.cuda(), w.cuda(), None if res is None else res.cuda())
+        aq, sa = w4.quantize_activations(y16 if res is None else y16[0])
+        assert torch.equal(aq, got[0]) and torch.equal(sa, got[1])
+    assert torch.equal(got[1].cpu(), s)
+    assert torch.equal(values, q.float() * s.repeat_interleave(128, 1))
+
+
+def test_strided_and_misaligned_rows():
+    for H, off in ((512, 0), (512, 1), (515, 3), (1536, 8)):
+        M = 6
+        g = torch.Generator().manual_seed(H + off)
+        wide = torch.randn(M, H + 40, generator=g)
+        big = torch.randn(M, H + 24, generator=g).to(BF16)
+        w = torch.randn(H + 8, generator=g)
+        x, res, ww = wide[:, off:off + H], big[:, off:off + H], w[off % 4:off % 4 + H]
+        log(f"rms_norm strided H={H} offset={off}")
+        y, r = w4.rms_norm(wide.cuda()[:, off:off + H], w.cuda()[off % 4:off % 4 + H], big.cuda()[:, off:off + H])
+        y0, r0 = w4.rms_norm(x.contiguous().cuda(), ww.contiguous().cuda(), res.contiguous().cuda())
+        assert torch.equal(y, y0) and torch.equal(r, r0)
+        if H % 128 == 0:
+            q, s, _ = w4.rms_norm(wide.cuda()[:, off:off + H], w.cuda()[off % 4:off % 4 + H],
+                                  big.cuda()[:, off:off + H], bits=8)
+            q0, s0, _ = w4.rms_norm(x.contiguous().cuda(), ww.contiguous().cuda(), res.contiguous().cuda(), bits=8)
+            assert torch.equal(q, q0) and torch.equal(s, s0)
+
+
+def test_extremes():
+    # a row of zeros, huge and tiny rows (their squares leave binary32), a row with an infinity
+    x = torch.ones(5, 256)
+    x[0] = 0
+    x[1] = 1e30
+    x[2] = 1e-30
+    x[3, 5] = float("inf")
+    x[4, 7] = float("nan")
+    w = torch.ones(256)
+    y = w4.rms_norm(x.cuda(), w.cuda(), eps=1e-6).cpu().float()
+    assert (y[0] == 0).all() and (y[1] == 1).all()
+    assert ((y[2] - 1e-27).abs() <= 1e-27 * 2.0 ** -7).all()   # eps rules: 1e-30 / sqrt(1e-6)
+    assert y[3, 5].isnan() and (y[3, :5] == 0).all() and y[4].isnan().all()
+
+
+def test_in_place_residual_empty_stream_and_refusals():
+    x, res, w = inputs(9, 640, F32, BF16, BF16, 5)
+    xd, rd, wd = x.cuda(), res.cuda(), w.cuda()
+    y0, r0 = w4.rms_norm(xd, wd, rd)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    kept = rd.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y1, r1 = w4.rms_norm(xd, wd, kept, residual_out=kept)
+    s.synchronize()
+    assert r1 is kept and torch.equal(y0, y1) and torch.equal(r0, r1)
+    assert w4.rms_norm(xd[:0], wd).shape == (0, 640)
+    for bad in (dict(weight=wd[:5]), dict(residual=rd[:2]), dict(residual=rd, residual_out=rd[:2]),
+                dict(residual_out=rd), dict(bits=3), dict(residual=rd, residual_out=rd.float())):
+        args = dict(x=xd, weight=wd)
+        args.update(bad)
+        with pytest.raises((ValueError, TypeError)):
+            w4.rms_norm(**args)
+    with pytest.raises(w4.W4Error):
+        w4.rms_norm(xd[:, :600], wd[:600], bits=8)        # not a multiple of 128
