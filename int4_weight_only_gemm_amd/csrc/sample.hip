@@ -9,21 +9,29 @@
 //     the kept weights passes u times their sum;  prob = w_token / that sum
 //
 // Which token a uniform number falls on is a comparison of long sums, so the weights are
-// computed in binary64 and summed as integers, in units of 2^-44 of the largest weight: integer
-// sums do not depend on the order of atomics, and the result is the same in every run.  2^19
-// weights of at most 2^44 stay below 2^63.
+// computed in binary64 and summed as integers, in units of 2^-44 of the largest weight: integer sums do not depend on the order
+// of atomics, and the result is the same in every run.  2^19 weights of at most 2^44 stay below
+// 2^63.
 //
 // Nothing is sorted.  Both cuts keep a prefix of the order, so the kept tokens are those up to
-// one (logit, index) pair.  Three passes over the logits, the second and third mostly from the
-// caches:
-//   1. the row's largest logit;
-//   2. counts and weight sums by bins of 1/128 nat below the largest (rows with a cut only):
-//      the bins in which the cuts fall;
-//   3. weight sums of the tokens above those bins, and the few tokens inside them (pairs in a
-//      list), whose exact ranks give the cut; then the token.
+// one (logit, index) pair, and what is usually kept lies among the row's few hundred largest.
+//   1. One pass over the logits finds the largest one and lists all tokens above a threshold
+//      that each chunk of the row takes from its first 4096 tokens so that about kWant of the row
+//      pass it.  Where top-k does not bound the sum, the chunk also sums all weights by tiles of
+//      1024 tokens, in binary64 and a fixed order.  The last workgroup of a row to arrive finds
+//      the cuts in the list and draws, if the list reaches them (or there are none: then from
+//      the tile sums): counts and weight sums by bins of 1/32 nat below the largest give the
+//      bins in which the cuts fall, and the exact ranks of the few tokens inside those bins the
+//      cut.  Then sums of kept weight by tiles give the tile of the token, which is read again.
+//   2., 3. Rows whose cuts lie deeper (flat distributions, large k, thousands of equal logits):
+//      the same from the whole row, one pass for the bins and one for what lies above and
+//      inside the cuts' bins.  Other rows' workgroups leave at once.
 // Each row is split into chunks over workgroups; the last workgroup of a row to arrive does
-// the row's serial part (at pass 2: scanning 4096 bins, at pass 3: the cut and the draw, which
-// re-reads one chunk).
+// the row's serial part.  Workgroups are small (4 waves) for its sake: with 16 waves each of its
+// steps took four times as long (one row of 152064: 26 us in all, 19 us with 4 waves).
+//
+// Measured: 160 rows of 152064 float32 logits with mixed settings 71 us for all three launches
+// (97 MB: one read at the rate of a large copy is 19 us), one row 24 us.
 #include "internal.h"
 
 using namespace w4host;
@@ -31,23 +39,34 @@ using namespace w4dev;
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 4096;            // the last one also takes all that lies further below
-constexpr float kBinsPerNat = 128.0f;  // 32 nats: a weight below 2^-46 of the largest rounds to 0
-constexpr int kList = 2048;            // tokens of the cuts' bins that a row's list holds
+constexpr int kBins = 1024;            // the last one also takes all that lies further below
+constexpr float kBinsPerNat = 32.0f;   // 32 nats: a weight below 2^-46 of the largest rounds to 0
+constexpr int kNear = 288;             // bins of the weights above e^-9
+constexpr int kTile = kThreads * 4;    // tokens a workgroup reads at a time
+constexpr int kAhead = 4;              // tiles in flight
+constexpr int kMinChunk = kAhead * kTile;
+constexpr int kMaxChunk = 60 * kTile;  // counts and sums of a chunk's far bins share 64 bits
+constexpr int kInside = 1024;          // tokens of the cuts' bins that pass 3's list holds
+constexpr int kWant = 512;             // tokens of a row that pass 1 aims to list
+constexpr int kListed = 2048;          // and the most that its chunks' lists hold together
+constexpr int kOwn = 1024;             // and that one chunk's list holds
 constexpr double kUnit = 17592186044416.0;  // 2^44
 constexpr int64_t kMaxV = 1 << 19;
-constexpr int kMaxChunks = 64;
-constexpr int64_t kRows = 1024;        // rows of one set of launches (their scratch is 50 KB each)
+constexpr int kMaxChunks = (int)(kMaxV / kMinChunk);
+constexpr int kMaxTiles = (int)(kMaxV / kTile);
+constexpr int64_t kRows = 1024;        // rows of one set of launches (their scratch is 40 KB each)
 
 // What pass 2 leaves for pass 3.
 struct RowCut {
+    int done;            // pass 1 has drawn the row's token
     int sure_end;        // bins below this are kept by top-k and top-p
     int lo, hi;          // bins in which the top-p cut may fall (lo > hi: none)
     int bin_k;           // bin of the top-k cut (-1: none)
     unsigned left_k;     // tokens that top-k keeps of bin_k
-    unsigned long long sum_before_lo, sum_before_k, sum_all;
+    unsigned long long sum_before_lo, sum_before_k;
+    double sum_all;
 };
 
 struct SampleParams {
@@ -59,13 +78,15 @@ struct SampleParams {
     int64_t stride;
     int V, chunks, chunk_len;
     // workspace
-    unsigned *arrive;            // [2][B], zero between calls
+    unsigned *arrive;            // [4][B], zero between calls: arrivals of the three passes, list length of pass 3
     unsigned long long *top;     // [B][kMaxChunks] largest (logit, index) of each chunk
-    unsigned long long *sums;    // [B][kMaxChunks] kept weight of each chunk, above the cuts' bins
+    float *bound;                // [B][kMaxChunks][2] pass 1: a chunk's threshold, and what its sums are relative to
+    unsigned *count;             // [B][kMaxChunks] pass 1: tokens in a chunk's list
+    double *tile_sum;            // [B][kMaxTiles] pass 1: all weight of each tile
+    unsigned long long *sums;    // [B][kMaxTiles] pass 3: kept weight of each tile, above the cuts' bins
     unsigned long long *hist_w;  // [B][kBins]
     unsigned *hist_n;            // [B][kBins]
-    unsigned long long *list;    // [B][kList]
-    unsigned *listed;            // [B]
+    unsigned long long *list;    // [B][kListed]; pass 1: a share for each chunk
     RowCut *cut;                 // [B]
 };
 
@@ -96,19 +117,17 @@ __device__ __forceinline__ float logit_of(unsigned long long place)
     return __builtin_bit_cast(float, b);
 }
 
-template <bool F32>
-__device__ __forceinline__ float logit_at(const void *row, int i)
-{
-    const float l = load_one<F32>(row, i);
-    return l == l ? l : -__builtin_huge_valf();  // a NaN is never drawn
-}
+constexpr float kNone = -__builtin_huge_valf();
+constexpr float kMost = 3.40282346638528859812e38f;
+
+// A NaN counts as -infinity (never drawn), +infinity as the largest finite number.
+__device__ __forceinline__ float tame(float l) { return __builtin_amdgcn_fmed3f(fmaxf(l, kNone), kNone, kMost); }
 
 // Four logits from element e (a multiple of 4), -inf past the end.
 template <bool F32, bool VEC>
 __device__ __forceinline__ f32x4 logits4(const void *row, int e, int end)
 {
-    const float none = -__builtin_huge_valf();
-    f32x4 v = {none, none, none, none};
+    f32x4 v = {kNone, kNone, kNone, kNone};
     if (VEC && e + 4 <= end) {
         if (F32) {
             v = *(const f32x4 *)((const float *)row + e);
@@ -116,83 +135,117 @@ __device__ __forceinline__ f32x4 logits4(const void *row, int e, int end)
             const u32x2 r = *(const u32x2 *)((const uint16_t *)row + e);
             v = f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (v[j] != v[j]) v[j] = none;
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (e + j < end) v[j] = logit_at<F32>(row, e + j);
+            if (e + j < end) v[j] = load_one<F32>(row, e + j);
     }
-    return v;
+    return f32x4{tame(v[0]), tame(v[1]), tame(v[2]), tame(v[3])};
 }
 
 struct Row {
     float top, bin_scale;
-    double inv_t;
+    double per_log2;  // log2(e) / T
     float min_p;
+    int near_bins;  // bins whose weights take the full series
 };
 
-// Bin of a logit: monotone in it, since each binary32 step is.
+// Bin of a logit: monotone in it, since each binary32 step is.  An infinite distance, or an
+// infinite one times a scale of 0, takes the last bin.
 __device__ __forceinline__ int bin_of(float l, const Row &r)
 {
-    if (l == r.top) return 0;
-    const float b = (r.top - l) * r.bin_scale;
-    return b < (float)(kBins - 1) ? (int)b : kBins - 1;  // infinite or NaN (infinity * 0): the last
+    return (int)fminf((r.top - l) * r.bin_scale, (float)(kBins - 1));
 }
 
-// exp((l - top) / T) of a logit outside the last bin, so the argument lies in (-33, 0].  The
-// same weight is computed in several places and has to come out with the same bits, so every
-// step is spelled out: x = n ln 2 + f with |f| <= ln 2 / 2, the exponential series of f to its
-// 12th power (the first term left out is below 2e-16), and n added to the exponent.
-__device__ __forceinline__ double weight_of(float l, const Row &r)
+// 2^x * 2^44 for |x| <= 1000; the weight of a logit outside the last bin, exp((l - top) / T), in
+// units.  The same weight is computed in several places and has to come out with the same bits,
+// so every step is spelled out: x = n + f with |f| <= 1/2, the series of 2^f = exp(f ln 2) to the
+// TERMS-th power, and n added to the exponent.  (n comes from an addition whose result has a last
+// bit of 1: the conversions that a rounding and a scaling instruction would need run at a quarter
+// of the rate.)
+constexpr double series_term(int i)
+{
+    double c = 1.0;
+    for (int k = 1; k <= i; ++k) c *= 0.69314718055994530942 / k;
+    return c;
+}
+template <int TERMS>
+__device__ __forceinline__ double exp2_units(double x)
 {
 #pragma clang fp contract(off)
-    if (l == r.top) return 1.0;
-    const double x = ((double)l - (double)r.top) * r.inv_t;
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    const double f = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, x));
-    double s = 1.0 / 479001600.0;
-    s = __builtin_fma(s, f, 1.0 / 39916800.0);
-    s = __builtin_fma(s, f, 1.0 / 3628800.0);
-    s = __builtin_fma(s, f, 1.0 / 362880.0);
-    s = __builtin_fma(s, f, 1.0 / 40320.0);
-    s = __builtin_fma(s, f, 1.0 / 5040.0);
-    s = __builtin_fma(s, f, 1.0 / 720.0);
-    s = __builtin_fma(s, f, 1.0 / 120.0);
-    s = __builtin_fma(s, f, 1.0 / 24.0);
-    s = __builtin_fma(s, f, 1.0 / 6.0);
-    s = __builtin_fma(s, f, 0.5);
-    s = __builtin_fma(s, f, 1.0);
-    s = __builtin_fma(s, f, 1.0);
-    return __builtin_ldexp(s, (int)n);
+    const double whole = x + 0x1.8p52, f = x - (whole - 0x1.8p52);  // x rounded, in the low bits of `whole`
+    constexpr double c[13] = {series_term(0), series_term(1), series_term(2), series_term(3), series_term(4),
+                              series_term(5), series_term(6), series_term(7), series_term(8), series_term(9),
+                              series_term(10), series_term(11), series_term(12)};
+    double s = c[TERMS];
+#pragma unroll
+    for (int i = TERMS - 1; i >= 0; --i) s = __builtin_fma(s, f, c[i]);
+    const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, whole) + 44;
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, s) + ((uint64_t)(uint32_t)n << 52));
 }
-// A weight in units of 2^-44 of the largest, and the same with min-p applied.
-__device__ __forceinline__ unsigned long long fixed(double w)
+// Out of line wherever it is not in a loop over the row: a copy is a third of a kilobyte, a
+// kernel would hold some sixty of them, and code that runs once a row waits for its lines.
+__device__ __noinline__ double full_series(double x) { return exp2_units<12>(x); }
+__device__ __noinline__ double short_series(double x) { return exp2_units<8>(x); }
+
+__device__ __forceinline__ double log2_of(float l, const Row &r) { return ((double)l - (double)r.top) * r.per_log2; }
+
+// A weight outside the last bin in units of 2^-44 of the largest, and the same with min-p
+// applied.  The first term left out of the series is below 2e-16 of the weight with 12 terms, and
+// with 8 below 2^-32 of it, which is below 2^-44 of the largest for the far bins, where most of
+// a vocabulary lies.  LOOP: in a loop over the row, the short series in line.
+__device__ __forceinline__ double weight_of(float l, const Row &r) { return full_series(log2_of(l, r)); }
+template <bool LOOP>
+__device__ __forceinline__ unsigned long long far_weight(float l, const Row &r)  // below 2^32
 {
-    return (unsigned long long)__builtin_fma(w, kUnit, 0.5);
+    const double x = log2_of(l, r);
+    return (uint32_t)((LOOP ? exp2_units<8>(x) : short_series(x)) + 0.5);
 }
-__device__ __forceinline__ unsigned long long drawn_weight(float l, const Row &r)
+template <bool LOOP = false>
+__device__ __forceinline__ unsigned long long fixed_weight(float l, int bin, const Row &r)
 {
+    return bin < r.near_bins ? (unsigned long long)(weight_of(l, r) + 0.5) : far_weight<LOOP>(l, r);
+}
+template <bool LOOP = false>
+__device__ __forceinline__ unsigned long long drawn_weight(float l, int bin, const Row &r)
+{
+    if (bin >= r.near_bins) return far_weight<LOOP>(l, r);
     const double w = weight_of(l, r);
-    return w >= (double)r.min_p ? fixed(w) : 0ull;
+    return w < (double)r.min_p * kUnit ? 0ull : (unsigned long long)(w + 0.5);
 }
 
-__device__ __forceinline__ unsigned long long wave_sum(unsigned long long v)
+// The steps of an inclusive scan over a wave's lanes: shifts within a DPP row of 16, then the
+// rows' last lanes passed on (to rows 1 and 3, then to the upper half).  Lane-to-lane moves through
+// LDS make a scan of 64 bits over ten times as long.
+template <typename F>
+__device__ __forceinline__ void lane_steps(F step)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    using all = std::integral_constant<int, 0xF>;
+    step(std::integral_constant<int, 0x111>{}, all{});                               // row_shr:1
+    step(std::integral_constant<int, 0x112>{}, all{});                               // row_shr:2
+    step(std::integral_constant<int, 0x114>{}, all{});                               // row_shr:4
+    step(std::integral_constant<int, 0x118>{}, all{});                               // row_shr:8
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast:15
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row_bcast:31
+}
+// Inclusive sum over the wave's lanes up to this one.
+__device__ __forceinline__ unsigned long long wave_scan(unsigned long long v)
+{
+    lane_steps([&](auto ctrl, auto rows) {
+        const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, decltype(ctrl)::value, decltype(rows)::value,
+                                                   0xF, false);
+        const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), decltype(ctrl)::value,
+                                                   decltype(rows)::value, 0xF, false);
+        v += (unsigned long long)(uint32_t)hi << 32 | (uint32_t)lo;
+    });
     return v;
 }
-__device__ __forceinline__ unsigned long long wave_scan(unsigned long long v, int lane)  // inclusive
+__device__ __forceinline__ unsigned long long lane_value(unsigned long long v, int lane)  // uniform lane
 {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const unsigned long long o = __shfl_up(v, off, 64);
-        if (lane >= off) v += o;
-    }
-    return v;
+    return (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
 }
+__device__ __forceinline__ unsigned long long wave_sum(unsigned long long v) { return lane_value(wave_scan(v), 63); }
 
 // Sum over the workgroup, in every thread.
 __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *s)
@@ -201,18 +254,24 @@ __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, un
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) v += s[i];
-    return v;
+    return s[0] + s[1] + s[2] + s[3];
+}
+__device__ __forceinline__ unsigned long long wave_min(unsigned long long v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        const int lo = __builtin_amdgcn_update_dpp(-1, (int)(uint32_t)v, decltype(ctrl)::value, decltype(rows)::value,
+                                                   0xF, false);
+        const int hi = __builtin_amdgcn_update_dpp(-1, (int)(uint32_t)(v >> 32), decltype(ctrl)::value,
+                                                   decltype(rows)::value, 0xF, false);
+        const unsigned long long o = (unsigned long long)(uint32_t)hi << 32 | (uint32_t)lo;
+        v = o < v ? o : v;
+    };
+    lane_steps(step);
+    return lane_value(v, 63);
 }
 __device__ __forceinline__ unsigned long long block_min(unsigned long long v, unsigned long long *s)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const unsigned long long o = __shfl_xor(v, off, 64);
-        v = o < v ? o : v;
-    }
+    v = wave_min(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -244,21 +303,37 @@ __device__ __forceinline__ bool last_to_arrive(unsigned *count, int chunks, unsi
 __device__ __forceinline__ unsigned long long row_top(const SampleParams &p, int b)
 {
     unsigned long long best = ~0ull;
-    for (int c = 0; c < p.chunks; ++c) {
+    for (int c = threadIdx.x & 63; c < p.chunks; c += 64) {
         const unsigned long long v = p.top[(int64_t)b * kMaxChunks + c];
         best = v < best ? v : best;
     }
-    return best;
+    return wave_min(best);
 }
 
-__device__ __forceinline__ Row row_of(const SampleParams &p, int b, float top, float t)
+// A row's settings, read together at a kernel's start so that their latencies overlap.
+struct Settings {
+    float t, top_p, min_p, u;
+    int k;
+};
+__device__ __forceinline__ Settings settings_of(const SampleParams &p, int b)
+{
+    Settings s;
+    s.t = p.temperature ? p.temperature[b] : 1.f;
+    s.top_p = p.top_p ? p.top_p[b] : 1.f;
+    s.min_p = p.min_p ? p.min_p[b] : 0.f;
+    s.k = p.top_k ? p.top_k[b] : 0;
+    s.u = p.u[b];
+    return s;
+}
+
+__device__ __forceinline__ Row row_of(const Settings &s, float top)
 {
     Row r;
     r.top = top;
-    r.inv_t = 1.0 / (double)t;
-    r.bin_scale = kBinsPerNat / t;
-    const float m = p.min_p ? p.min_p[b] : 0.f;
-    r.min_p = m > 0.f ? fminf(m, 1.f) : 0.f;
+    r.per_log2 = 1.4426950408889634 / (double)s.t;
+    r.bin_scale = fminf(kBinsPerNat / s.t, kMost);
+    r.min_p = s.min_p > 0.f ? fminf(s.min_p, 1.f) : 0.f;
+    r.near_bins = r.min_p > 0.f ? kBins : kNear;
     return r;
 }
 
@@ -267,36 +342,519 @@ __device__ __forceinline__ const void *row_ptr(const SampleParams &p, int b, boo
     return (const char *)p.logits + (int64_t)b * p.stride * (f32 ? 4 : 2);
 }
 
+constexpr int kPer = kBins / kThreads;
+
+// The bins in which the cuts fall, from each thread's kPer bins (n: counts, w: weight sums).
+// `all`: the row's weight where top-k does not bound it.  *cut is in LDS; ends with a barrier.
+struct FindBins {
+    unsigned long long w[kWaves], w1[2];
+    unsigned n[kWaves];
+};
+__device__ __forceinline__ void find_bins(const unsigned (&n)[kPer], const unsigned long long (&w)[kPer], int k,
+                                          float top_p, int V, bool sum_is_all, double all, RowCut *cut, FindBins *s)
+{
+    const bool cut_k = k > 0 && k < V, cut_p = top_p < 1.f;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    unsigned n_own = 0, n_before;
+    unsigned long long w_own = 0, w_before;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        n_own += n[i];
+        w_own += w[i];
+    }
+    w_before = wave_scan(w_own);
+    n_before = (unsigned)wave_scan(n_own);
+    if (lane == 63) {
+        s->w[wave] = w_before;
+        s->n[wave] = n_before;
+    }
+    if (tid == 0) cut->bin_k = -1, cut->lo = kBins, cut->hi = cut_p ? kBins : -1;
+    __syncthreads();
+    unsigned long long w_all = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i < wave) {
+            w_before += s->w[i];
+            n_before += s->n[i];
+        }
+        w_all += s->w[i];
+    }
+    n_before -= n_own;
+    w_before -= w_own;
+    if (sum_is_all) all = (double)w_all;
+    // the bin in which the k-th token lies (none: it lies where nothing weighs anything), and the
+    // least and the most weight that top-k may keep
+    if (tid == 0) s->w1[0] = s->w1[1] = 0ull;
+    __syncthreads();
+    if (cut_k) {
+        unsigned nb = n_before;
+        unsigned long long wb = w_before;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (nb < (unsigned)k && nb + n[i] >= (unsigned)k) {
+                cut->bin_k = tid * kPer + i;
+                cut->left_k = (unsigned)k - nb;
+                cut->sum_before_k = wb;
+                s->w1[0] = wb;
+                s->w1[1] = wb + w[i];
+            }
+            nb += n[i];
+            wb += w[i];
+        }
+    }
+    __syncthreads();
+    if (cut_p) {
+        const double pp = (double)fmaxf(top_p, 0.f);
+        const bool by_k = cut->bin_k >= 0;
+        const double want0 = pp * (by_k ? (double)s->w1[0] : all), want1 = pp * (by_k ? (double)s->w1[1] : all);
+        unsigned long long wb = w_before;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const double before = (double)wb, through = (double)(wb + w[i]);
+            const int bin = tid * kPer + i;
+            if ((before < want0 || bin == 0) && through >= want0) {
+                cut->lo = bin;
+                cut->sum_before_lo = wb;
+            }
+            if ((before < want1 || bin == 0) && through >= want1) cut->hi = bin;
+            wb += w[i];
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const int of_k = cut->bin_k >= 0 ? cut->bin_k : kBins;
+        cut->sure_end = cut_p ? min(cut->lo, of_k) : of_k;
+        cut->sum_all = all;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ bool inside(int bin, const RowCut &c)
+{
+    return (bin >= c.lo && bin <= c.hi) || bin == c.bin_k;
+}
+
+// The tokens inside the cuts' bins, up to N of them.
+template <int N>
+struct Inside {
+    unsigned long long place[N], weight[N], before[N];
+    unsigned rank[N];
+    uint8_t in[N];  // 1: in the bin of the top-k cut, 2: in those of the top-p cut
+};
+template <int N>
+__device__ __forceinline__ void put_inside(Inside<N> &s, unsigned i, unsigned long long at, const RowCut &cut,
+                                           const Row &r)
+{
+    const float l = logit_of(at);
+    const int bin = bin_of(l, r);
+    s.place[i] = at;
+    s.weight[i] = fixed_weight(l, bin, r);
+    s.in[i] = (bin == cut.bin_k ? 1 : 0) | (bin >= cut.lo && bin <= cut.hi ? 2 : 0);
+    s.rank[i] = 0u;
+    s.before[i] = 0ull;
+}
+
+// The last place that is kept of n such tokens (0: none of them), from each one's exact rank and
+// the weight before it: every token is compared with every other one, `parts` threads a token,
+// each with a share of the others.  Begins and ends with a barrier.
+template <int N>
+__device__ __forceinline__ unsigned long long cut_of(Inside<N> &t, unsigned n, const RowCut &cut, float top_p,
+                                                     unsigned long long best, unsigned long long *s)
+{
+    const unsigned tid = threadIdx.x;
+    const bool cut_p = top_p < 1.f;
+    __syncthreads();
+    const unsigned width = n <= 64 ? 64 : 1u << (32 - __builtin_clz(n - 1));
+    const unsigned parts = width <= kThreads ? kThreads / width : 1;
+    const unsigned share = (n + parts - 1) / parts;
+    for (unsigned i = tid % width; i < n; i += kThreads) {
+        const unsigned from = (tid / width) * share, to = min(n, from + share);
+        const unsigned long long at = t.place[i];
+        unsigned rank = 0;
+        unsigned long long sum = 0;
+        for (unsigned o = from; o < to; ++o) {
+            const bool earlier = t.place[o] < at;
+            rank += earlier && (t.in[o] & 1);
+            sum += earlier && (t.in[o] & 2) ? t.weight[o] : 0ull;
+        }
+        if (rank) atomicAdd(&t.rank[i], rank);
+        if (sum) atomicAdd(&t.before[i], sum);
+    }
+    __syncthreads();
+    unsigned long long w1 = 0;
+    for (unsigned i = tid; i < n; i += kThreads)
+        if ((t.in[i] & 1) && t.rank[i] < cut.left_k) w1 += t.weight[i];
+    w1 = block_sum(w1, s);
+    const double want =
+        (double)fmaxf(top_p, 0.f) * (cut.bin_k >= 0 ? (double)(cut.sum_before_k + w1) : cut.sum_all);
+    unsigned long long kept = 0;
+    for (unsigned i = tid; i < n; i += kThreads) {
+        bool keep = !(t.in[i] & 1) || t.rank[i] < cut.left_k;
+        if (cut_p)
+            keep = keep && (t.in[i] & 2) && ((double)(cut.sum_before_lo + t.before[i]) < want || t.place[i] == best);
+        if (keep && t.place[i] > kept) kept = t.place[i];
+    }
+    return ~block_min(~kept, s);
+}
+
+// The integer target of u in [0, total): the token drawn is the first whose running sum exceeds it.
+// A u of 1 or more, or one that rounds up to it, takes the last token that weighs anything.
+__device__ __forceinline__ unsigned long long target_of(float u, unsigned long long total)
+{
+    const double real = u > 0.f ? (double)u * (double)total : 0.0;
+    const unsigned long long t = real < (double)total ? (unsigned long long)real : total;
+    return t < total ? t : total - 1;
+}
+
+// The tile of s_sum in which the running sum passes the target (what is left of it in *target).
+__device__ __forceinline__ int pick_tile(const unsigned long long *s_sum, int tiles, unsigned long long *target)
+{
+    const int lane = threadIdx.x & 63;
+    unsigned long long before = 0;
+    for (int i = 0; i < tiles; i += 64) {
+        const unsigned long long own = i + lane < tiles ? s_sum[i + lane] : 0ull;
+        const unsigned long long run = before + wave_scan(own);
+        const unsigned long long hit = __ballot(run > *target);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            *target -= lane_value(run - own, at);
+            return i + at;
+        }
+        before = lane_value(run, 63);
+    }
+    return 0;  // not reached: the target is below the sum
+}
+
+// Draws from the sums of kept weight by tiles: the tile, then its token.  Kept: the bins below
+// sure_end, and the places up to last_place.  Begins with a barrier.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void draw_token(const SampleParams &p, int b, const void *row, const Row &r, float u,
+                                           int sure_end, unsigned long long last_place,
+                                           const unsigned long long *s_sum, int tiles, unsigned long long *s)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __syncthreads();
+    unsigned long long total = 0;
+    for (int i = lane; i < tiles; i += 64) total += s_sum[i];
+    total = wave_sum(total);
+    unsigned long long target = target_of(u, total);
+    const int e = pick_tile(s_sum, tiles, &target) * kTile + tid * 4;
+    const f32x4 l = logits4<F32, VEC>(row, e, p.V);
+    unsigned long long w[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int bin = bin_of(l[j], r);
+        w[j] = bin == kBins - 1 || (bin >= sure_end && place_of(l[j], e + j) > last_place) ? 0ull
+                                                                                           : drawn_weight(l[j], bin, r);
+        mine += w[j];
+    }
+    unsigned long long run = wave_scan(mine);
+    __syncthreads();
+    if (lane == 63) s[wave] = run;
+    __syncthreads();
+    run -= mine;
+    for (int i = 0; i < wave; ++i) run += s[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (run <= target && target < run + w[j]) {
+            p.token[b] = e + j;
+            if (p.prob) p.prob[b] = (float)(weight_of(l[j], r) / (double)total);
+        }
+        run += w[j];
+    }
+}
+
 // ------------------------------------------------------------------------------------
-// Pass 1: each chunk's largest (logit, lowest index); the row's bins cleared.
+// Pass 1: the largest logit, the list, and most rows' tokens.
 
 template <bool F32, bool VEC>
-__global__ __launch_bounds__(kThreads) void sample_top_kernel(const SampleParams p, bool clear)
+__global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParams p)
 {
+    struct Hist {
+        unsigned long long w[kBins];
+        unsigned n[kBins];
+    };
+    union Work {
+        Hist hist;                   // dead once its bins are in registers
+        Inside<kInside / 2> inside;
+    };
+    __shared__ unsigned long long s_place[kOwn];
+    __shared__ Work s_work;
+    __shared__ union {
+        double all[kMaxTiles];                // last workgroup: the weight of each tile
+        unsigned long long kept[kMaxTiles];   // and, once that is done with, its kept weight
+    } s_tiles;
+    double (&s_tile)[kMaxTiles] = s_tiles.all;
+    unsigned long long (&s_sum)[kMaxTiles] = s_tiles.kept;
+    __shared__ double s_part[kMaxChunk / kTile][kWaves];
+    __shared__ __align__(16) float s_group[kThreads];
     __shared__ unsigned long long s[kWaves];
-    const int c = blockIdx.x, b = blockIdx.y;
+    __shared__ float s_bound[2 * kWaves];
+    __shared__ FindBins s_find;
+    __shared__ RowCut s_cut;
+    __shared__ unsigned s_count, s_inside, s_last;
+    const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int begin = c * p.chunk_len, end = min(p.V, begin + p.chunk_len);
     const void *row = row_ptr(p, b, F32);
-    unsigned long long best = ~0ull;
-#pragma unroll 4
-    for (int e = begin + threadIdx.x * 4; e < end; e += kThreads * 4) {
-        const f32x4 l = logits4<F32, VEC>(row, e, end);
+    f32x4 ahead[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const unsigned long long v = place_of(l[j], e + j);
-            best = v < best ? v : best;
+    for (int i = 0; i < kAhead; ++i) ahead[i] = logits4<F32, VEC>(row, begin + i * kTile + tid * 4, end);
+    const Settings set = settings_of(p, b);
+    const bool cut_k = set.k > 0 && set.k < p.V, cut_p = set.top_p < 1.f, greedy = !(set.t > 0.f);
+    const bool sum_all = !greedy && !cut_k && (cut_p || !(set.min_p > 0.f));
+    const double per_log2 = greedy ? 0.0 : 1.4426950408889634 / (double)set.t;
+
+    // The threshold, from the chunk's first tiles: each thread's largest of 16 tokens, the wave's
+    // q-th largest of those 64, and the second smallest of the waves' four (the largest, where a
+    // wave has too few).  Any value would do: it only sets how many tokens are listed.  Short
+    // rows list all.
+    const int tiles = (p.V + kTile - 1) / kTile;
+    float own = ahead[0][0];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) own = fmaxf(own, ahead[i][j]);
+    s_group[tid] = own;
+    if (tid == 0) s_count = 0u;
+    if (lane == 0) s_bound[wave] = kNone;
+    __syncthreads();
+    const int q = p.V <= kOwn ? 0 : min(32, max(2, kWant * kAhead / (tiles * kWaves)));
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < 64; i += 4) {
+        const f32x4 o = *(const f32x4 *)(s_group + wave * 64 + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) above += o[j] > own || (o[j] == own && i + j < lane);
+    }
+    if (above == q - 1) s_bound[wave] = own;
+    if (above == 0) s_bound[kWaves + wave] = own;
+    __syncthreads();
+    const float b0 = fminf(s_bound[0], s_bound[1]), b1 = fmaxf(s_bound[0], s_bound[1]);
+    const float b2 = fminf(s_bound[2], s_bound[3]), b3 = fmaxf(s_bound[2], s_bound[3]);
+    const float bound = fminf(b0, b2) == kNone ? fmaxf(b1, b3) : fminf(fmaxf(b0, b2), fminf(b1, b3));
+    float ref = fmaxf(fmaxf(s_bound[4], s_bound[5]), fmaxf(s_bound[6], s_bound[7]));
+    ref = ref == kNone ? 0.f : ref;
+
+    unsigned long long best = ~0ull;
+    for (int e0 = begin; e0 < end; e0 += kTile) {
+        const int e = e0 + tid * 4;
+        const f32x4 l = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = logits4<F32, VEC>(row, e + kAhead * kTile, end);
+        const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+        if (most >= bound && most != kNone) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (l[j] < bound || l[j] == kNone) continue;
+                const unsigned long long at = place_of(l[j], e + j);
+                best = at < best ? at : best;
+                if (greedy) continue;
+                const unsigned i = atomicAdd(&s_count, 1u);
+                if (i < kOwn) s_place[i] = at;
+            }
+        }
+        if (sum_all) {
+            double x[4], w = 0.0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = fmin(fmax(((double)l[j] - (double)ref) * per_log2, -1000.0), 900.0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w += exp2_units<10>(x[j]);  // within 2^-42
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) w += __shfl_xor(w, off, 64);
+            if (lane == 0) s_part[(e0 - begin) / kTile][wave] = w;
         }
     }
     best = block_min(best, s);
-    if (threadIdx.x == 0) p.top[(int64_t)b * kMaxChunks + c] = best;
-    if (clear) {
-        const int share = (kBins + p.chunks - 1) / p.chunks;
-        for (int i = c * share + threadIdx.x; i < min(kBins, (c + 1) * share); i += kThreads) {
-            p.hist_w[(int64_t)b * kBins + i] = 0ull;
-            p.hist_n[(int64_t)b * kBins + i] = 0u;
+    const int own_tiles = (end - begin + kTile - 1) / kTile;
+    if (sum_all && tid < own_tiles) {
+        double w = 0.0;
+        for (int i = 0; i < kWaves; ++i) w += s_part[tid][i];
+        put(p.tile_sum + (int64_t)b * kMaxTiles + begin / kTile + tid, w);
+    }
+    const unsigned room = min(kOwn, kListed / p.chunks), count = s_count;  // a chunk's place in the list
+    if (tid == 0) {
+        put(p.top + (int64_t)b * kMaxChunks + c, best);
+        // a list that is too long is none: no logit reaches its threshold
+        put(p.bound + ((int64_t)b * kMaxChunks + c) * 2, count <= room ? bound : __builtin_huge_valf());
+        put(p.bound + ((int64_t)b * kMaxChunks + c) * 2 + 1, ref);
+        put(p.count + (int64_t)b * kMaxChunks + c, min(count, room));
+    }
+    for (unsigned i = tid; i < min(count, room); i += kThreads)
+        put(p.list + (int64_t)b * kListed + c * room + i, s_place[i]);
+    if (!last_to_arrive(p.arrive + b, p.chunks, &s_last)) return;
+
+    // All that the row's workgroups left, read together.  What the lists hold past their lengths is
+    // not used.
+    unsigned long long place[kListed / kThreads];
+#pragma unroll
+    for (int i = 0; i < kListed / kThreads; ++i) place[i] = get(p.list + (int64_t)b * kListed + i * kThreads + tid);
+    bool mine[kListed / kThreads];
+#pragma unroll
+    for (int i = 0; i < kListed / kThreads; ++i) {
+        const unsigned at = i * kThreads + tid, chunk = at / room;
+        mine[i] = chunk < (unsigned)p.chunks && at - chunk * room < get(p.count + (int64_t)b * kMaxChunks + chunk);
+    }
+    best = ~0ull;
+    float least = kNone;
+    for (int i = lane; i < p.chunks; i += 64) {
+        const unsigned long long v = get(p.top + (int64_t)b * kMaxChunks + i);
+        best = v < best ? v : best;
+        least = fmaxf(least, get(p.bound + ((int64_t)b * kMaxChunks + i) * 2));
+    }
+    best = wave_min(best);
+    least = logit_of(wave_min(place_of(least, 0)));
+    const float top = best == ~0ull ? kNone : logit_of(best);
+    if (tid == 0) {
+        s_count = 0u;
+        p.cut[b].done = 1;
+    }
+    if (greedy || top == kNone) {  // the largest, or nothing to draw
+        if (tid == 0) {
+            p.token[b] = top == kNone ? -1 : (int32_t)(uint32_t)best;
+            if (p.prob) p.prob[b] = top == kNone ? 0.f : 1.f;
+        }
+        return;
+    }
+    const Row r = row_of(set, top);
+    double all = 0.0;  // the row's weight in units
+    bool settled = true;
+    if (sum_all) {
+        for (int i = tid; i < tiles; i += kThreads) {
+            const int chunk = i * kTile / p.chunk_len;
+            const double from = (double)get(p.bound + ((int64_t)b * kMaxChunks + chunk) * 2 + 1);
+            const double x = fmin(fmax((from - (double)top) * r.per_log2, -1000.0), 900.0);
+            s_tile[i] = get(p.tile_sum + (int64_t)b * kMaxTiles + i) * (full_series(x) * (1.0 / kUnit));
+        }
+        __syncthreads();
+        for (int i = lane; i < tiles; i += 64) all += s_tile[i];
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off, 64);
+        settled = all >= 0.5 * kUnit && all < 0x1p100;  // a chunk far above its first tiles overflows
+    }
+    if (!cut_k && !cut_p && !(r.min_p > 0.f)) {
+        // No cut: the tile in which the running sum passes the target, then the token.
+        if (settled) {
+            const double u = set.u > 0.f ? (double)set.u : 0.0;
+            double target = u * all;
+            int pick = 0, last = 0;
+            for (int i = lane; i < tiles; i += 64)
+                if (s_tile[i] > 0.0) last = i;  // the last tile that weighs anything
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) last = max(last, __shfl_xor(last, off, 64));
+            while (pick < last && target >= s_tile[pick]) target -= s_tile[pick++];
+            const int e = pick * kTile + tid * 4;
+            const f32x4 l = logits4<F32, VEC>(row, e, p.V);
+            unsigned long long w[4], mine = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int bin = bin_of(l[j], r);
+                w[j] = bin == kBins - 1 ? 0ull : fixed_weight(l[j], bin, r);
+                mine += w[j];
+            }
+            unsigned long long run = wave_scan(mine);
+            __syncthreads();
+            if (lane == 63) s[wave] = run;
+            __syncthreads();
+            run -= mine;
+            unsigned long long whole = 0;
+            for (int i = 0; i < kWaves; ++i) {
+                if (i < wave) run += s[i];
+                whole += s[i];
+            }
+            // the tile's tokens in units against a target in binary64: past the last by rounding at most
+            unsigned long long goal = (unsigned long long)fmin(target, 0x1p62);
+            if (goal >= whole) goal = whole - 1;
+            if (whole == 0) {
+                if (tid == 0) p.cut[b].done = 0;  // a tile below the units: left to the general passes
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (run <= goal && goal < run + w[j]) {
+                        p.token[b] = e + j;
+                        if (p.prob) p.prob[b] = (float)(weight_of(l[j], r) / all);
+                    }
+                    run += w[j];
+                }
+                return;
+            }
+        } else if (tid == 0) {
+            p.cut[b].done = 0;
+        }
+        return;
+    }
+
+    // The tokens above every chunk's threshold, one behind the other: the list is complete down to
+    // there.
+    for (int i = tid; i < kBins; i += kThreads) {
+        s_work.hist.w[i] = 0ull;
+        s_work.hist.n[i] = 0u;
+    }
+    __syncthreads();
+    for (int i = tid; i < tiles; i += kThreads) s_sum[i] = 0ull;
+#pragma unroll
+    for (int i = 0; i < kListed / kThreads; ++i) {
+        if (!mine[i] || logit_of(place[i]) < least) continue;
+        const unsigned at = atomicAdd(&s_count, 1u);
+        if (at < kOwn) s_place[at] = place[i];
+    }
+    __syncthreads();
+    const unsigned n = s_count;
+    const bool whole_row = least == kNone;
+    settled = settled && n > 0 && n <= kOwn && (whole_row || !cut_k || n >= (unsigned)set.k);
+    if (settled && !cut_k && !cut_p)  // min-p alone: does the list reach below it
+        settled = whole_row || bin_of(least, r) == kBins - 1 ||
+                  weight_of(least, r) < (double)r.min_p * kUnit * (1.0 - 1e-9);
+    if (settled) {
+        unsigned long long last_place = ~0ull;
+        int sure_end = kBins;
+        if (cut_k || cut_p) {
+            for (unsigned i = tid; i < n; i += kThreads) {
+                const float l = logit_of(s_place[i]);
+                const int bin = bin_of(l, r);
+                if (bin == kBins - 1) continue;
+                atomicAdd(&s_work.hist.n[bin], 1u);
+                atomicAdd(&s_work.hist.w[bin], fixed_weight(l, bin, r));
+            }
+            if (tid == 0) s_inside = 0u;
+            __syncthreads();
+            unsigned nb[kPer];
+            unsigned long long wb[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) nb[i] = s_work.hist.n[tid * kPer + i], wb[i] = s_work.hist.w[tid * kPer + i];
+            find_bins(nb, wb, set.k, set.top_p, p.V, whole_row || cut_k, all, &s_cut, &s_find);
+            const RowCut cut = s_cut;
+            sure_end = cut.sure_end;
+            settled = !cut_p || cut.lo < kBins;  // top-p alone: the list has to reach its cut
+            if (settled && (cut.bin_k >= 0 || cut.hi >= 0)) {
+                for (unsigned i = tid; i < n; i += kThreads) {
+                    if (!inside(bin_of(logit_of(s_place[i]), r), cut)) continue;
+                    const unsigned at = atomicAdd(&s_inside, 1u);
+                    if (at < kInside / 2) put_inside(s_work.inside, at, s_place[i], cut, r);
+                }
+                __syncthreads();
+                const unsigned in = s_inside;
+                settled = in <= kInside / 2;
+                if (settled) last_place = cut_of(s_work.inside, in, cut, set.top_p, best, s);
+            }
+        }
+        if (settled) {
+            for (unsigned i = tid; i < n; i += kThreads) {
+                const float l = logit_of(s_place[i]);
+                const int bin = bin_of(l, r);
+                if (bin != kBins - 1 && (bin < sure_end || s_place[i] <= last_place))
+                    atomicAdd(&s_sum[(uint32_t)s_place[i] / kTile], drawn_weight(l, bin, r));
+            }
+            draw_token<F32, VEC>(p, b, row, r, set.u, sure_end, last_place, s_sum, tiles, s);
+            return;
         }
     }
-    if (c == 0 && threadIdx.x == 0) p.listed[b] = 0u;
+    // Left to the general passes: their bins start at zero.
+    for (int i = tid; i < kBins; i += kThreads) {
+        p.hist_w[(int64_t)b * kBins + i] = 0ull;
+        p.hist_n[(int64_t)b * kBins + i] = 0u;
+    }
+    if (tid == 0) p.cut[b].done = 0;
 }
 
 // ------------------------------------------------------------------------------------
@@ -305,132 +863,65 @@ __global__ __launch_bounds__(kThreads) void sample_top_kernel(const SampleParams
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void sample_bins_kernel(const SampleParams p)
 {
+    // bins of large weights: sum and count; the far ones: sum below bit 48, count above
     __shared__ unsigned long long s_w[kBins];
-    __shared__ unsigned s_n[kBins];
-    __shared__ unsigned long long s_scan[kWaves];
-    __shared__ unsigned s_scan_n[kWaves];
+    __shared__ unsigned s_n[kNear];
+    __shared__ FindBins s_find;
+    __shared__ RowCut s_cut;
     __shared__ unsigned s_last;
-    __shared__ int s_bin_k, s_lo, s_hi;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const float t = p.temperature ? p.temperature[b] : 1.f;
-    const int k = p.top_k ? p.top_k[b] : 0;
-    const float top_p = p.top_p ? p.top_p[b] : 1.f;
-    const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
-    if (!(t > 0.f) || (!cut_k && !cut_p)) return;  // no cut in this row
-    const float top = logit_of(row_top(p, b));
-    if (top == -__builtin_huge_valf()) return;     // nothing to draw
-    const Row r = row_of(p, b, top, t);
-    for (int i = tid; i < kBins; i += kThreads) {
-        s_w[i] = 0ull;
-        s_n[i] = 0u;
-    }
-    __syncthreads();
+    if (p.cut[b].done) return;
+    const Settings set = settings_of(p, b);
     const int begin = c * p.chunk_len, end = min(p.V, begin + p.chunk_len);
     const void *row = row_ptr(p, b, F32);
-    for (int e = begin + tid * 4; e < end; e += kThreads * 4) {
-        const f32x4 l = logits4<F32, VEC>(row, e, end);
+    f32x4 ahead = logits4<F32, VEC>(row, begin + tid * 4, end);
+    const float top = logit_of(row_top(p, b));
+    const int k = set.k;
+    const float top_p = set.top_p;
+    const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
+    if (!cut_k && !cut_p) return;  // nothing to find
+    const Row r = row_of(set, top);
+    for (int i = tid; i < kBins; i += kThreads) {
+        s_w[i] = 0ull;
+        if (i < kNear) s_n[i] = 0u;
+    }
+    __syncthreads();
+    for (int e = begin + tid * 4; e < end; e += kTile) {
+        const f32x4 l = ahead;
+        ahead = logits4<F32, VEC>(row, e + kTile, end);  // -infinity past the end: the last bin
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (e + j >= end) break;
             const int bin = bin_of(l[j], r);
-            if (bin == kBins - 1) continue;  // weighs nothing; counted as the rest
-            atomicAdd(&s_n[bin], 1u);
-            if (cut_p) atomicAdd(&s_w[bin], fixed(weight_of(l[j], r)));
+            if (bin < kNear) {
+                atomicAdd(&s_n[bin], 1u);
+                if (cut_p) atomicAdd(&s_w[bin], fixed_weight(l[j], bin, r));
+            } else if (bin < kBins - 1) {  // the last weighs nothing and needs no count
+                atomicAdd(&s_w[bin], (1ull << 48) | (cut_p ? fixed_weight<true>(l[j], bin, r) : 0ull));
+            }
         }
     }
     __syncthreads();
     for (int i = tid; i < kBins; i += kThreads) {
-        if (!s_n[i]) continue;
-        __hip_atomic_fetch_add(p.hist_n + (int64_t)b * kBins + i, s_n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const unsigned n = i < kNear ? s_n[i] : (unsigned)(s_w[i] >> 48);
+        if (!n) continue;
+        __hip_atomic_fetch_add(p.hist_n + (int64_t)b * kBins + i, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (cut_p)
-            __hip_atomic_fetch_add(p.hist_w + (int64_t)b * kBins + i, s_w[i], __ATOMIC_RELAXED,
+            __hip_atomic_fetch_add(p.hist_w + (int64_t)b * kBins + i,
+                                   i < kNear ? s_w[i] : s_w[i] & ((1ull << 48) - 1), __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (!last_to_arrive(p.arrive + b, p.chunks, &s_last)) return;
+    if (!last_to_arrive(p.arrive + gridDim.y + b, p.chunks, &s_last)) return;
 
-    // four bins a thread: exclusive sums before them
-    constexpr int kPer = kBins / kThreads;
-    const int lane = tid & 63, wave = tid >> 6;
-    unsigned n[kPer], n_before = 0;
-    unsigned long long w[kPer], w_before = 0;
+    unsigned n[kPer];
+    unsigned long long w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         n[i] = get(p.hist_n + (int64_t)b * kBins + tid * kPer + i);
         w[i] = cut_p ? get(p.hist_w + (int64_t)b * kBins + tid * kPer + i) : 0ull;
-        n_before += n[i];
-        w_before += w[i];
     }
-    const unsigned n_own = n_before;
-    const unsigned long long w_own = w_before;
-    w_before = wave_scan(w_before, lane);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const unsigned o = (unsigned)__shfl_up((int)n_before, off, 64);
-        if (lane >= off) n_before += o;
-    }
-    if (lane == 63) {
-        s_scan[wave] = w_before;
-        s_scan_n[wave] = n_before;
-    }
-    if (tid == 0) s_bin_k = -1, s_lo = kBins, s_hi = kBins;
-    __syncthreads();
-    unsigned long long w_all = 0;
-    for (int i = 0; i < kWaves; ++i) {
-        if (i < wave) {
-            w_before += s_scan[i];
-            n_before += s_scan_n[i];
-        }
-        w_all += s_scan[i];
-    }
-    n_before -= n_own;
-    w_before -= w_own;
-    RowCut *cut = p.cut + b;
-    if (tid == 0) cut->sum_all = w_all;
-    // the bin in which the k-th token lies (none: it lies where nothing weighs anything)
-    __shared__ unsigned long long s_w1[2];
-    if (tid == 0) s_w1[0] = s_w1[1] = w_all;
-    __syncthreads();
-    if (cut_k) {
-        unsigned nb = n_before;
-        unsigned long long wb = w_before;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (nb < (unsigned)k && nb + n[i] >= (unsigned)k) {
-                s_bin_k = tid * kPer + i;
-                cut->left_k = (unsigned)k - nb;
-                cut->sum_before_k = wb;
-                s_w1[0] = wb;
-                s_w1[1] = wb + w[i];
-            }
-            nb += n[i];
-            wb += w[i];
-        }
-    }
-    __syncthreads();
-    // the bins in which the top-p cut lies, for the least and the most that top-k may keep
-    if (cut_p) {
-        const double pp = (double)fmaxf(top_p, 0.f);
-        const double want0 = pp * (double)s_w1[0], want1 = pp * (double)s_w1[1];
-        unsigned long long wb = w_before;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const double before = (double)wb, through = (double)(wb + w[i]);
-            const int bin = tid * kPer + i;
-            if ((before < want0 || bin == 0) && through >= want0) {
-                s_lo = bin;
-                cut->sum_before_lo = wb;
-            }
-            if ((before < want1 || bin == 0) && through >= want1) s_hi = bin;
-            wb += w[i];
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        cut->bin_k = s_bin_k;
-        cut->lo = cut_p ? s_lo : kBins;
-        cut->hi = cut_p ? s_hi : -1;
-        cut->sure_end = cut_p ? (s_bin_k >= 0 ? min(s_lo, s_bin_k) : s_lo) : (s_bin_k >= 0 ? s_bin_k : kBins);
-    }
+    if (tid == 0) s_cut.done = 0;
+    find_bins(n, w, k, top_p, p.V, true, 0.0, &s_cut, &s_find);
+    if (tid == 0) p.cut[b] = s_cut;
 }
 
 // ------------------------------------------------------------------------------------
@@ -439,112 +930,76 @@ __global__ __launch_bounds__(kThreads) void sample_bins_kernel(const SampleParam
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParams p)
 {
-    __shared__ unsigned long long s_place[kList];
-    __shared__ unsigned long long s_wt[kList];
-    __shared__ uint8_t s_in[kList];  // 1: in the bin of the top-k cut, 2: in those of the top-p cut
+    __shared__ Inside<kInside> s_inside;
+    __shared__ unsigned long long s_sum[kMaxTiles];
     __shared__ unsigned long long s[kWaves];
     __shared__ unsigned s_count, s_base, s_last;
-    const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const float none = -__builtin_huge_valf();
-    const unsigned long long best = row_top(p, b);
-    const float top = logit_of(best);
-    const float t = p.temperature ? p.temperature[b] : 1.f;
-    if (top == none || !(t > 0.f)) {  // nothing to draw, or the largest
-        if (c == 0 && tid == 0) {
-            p.token[b] = top == none ? -1 : (int32_t)(uint32_t)best;
-            if (p.prob) p.prob[b] = top == none ? 0.f : 1.f;
-        }
-        return;
-    }
-    const int k = p.top_k ? p.top_k[b] : 0;
-    const float top_p = p.top_p ? p.top_p[b] : 1.f;
-    const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
-    const Row r = row_of(p, b, top, t);
-    RowCut cut;
-    if (cut_k || cut_p)
-        cut = p.cut[b];
-    else
-        cut.sure_end = kBins, cut.lo = kBins, cut.hi = -1, cut.bin_k = -1;
-    auto inside = [&](int bin) { return (bin >= cut.lo && bin <= cut.hi) || bin == cut.bin_k; };
+    const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    RowCut cut = p.cut[b];  // its bins: only meaningful for a row with a cut
+    if (cut.done) return;
+    const Settings set = settings_of(p, b);
     const int begin = c * p.chunk_len, end = min(p.V, begin + p.chunk_len);
     const void *row = row_ptr(p, b, F32);
+    f32x4 ahead = logits4<F32, VEC>(row, begin + tid * 4, end);
+    const unsigned long long best = row_top(p, b);
+    const float top = logit_of(best);
+    const int k = set.k;
+    const float top_p = set.top_p;
+    const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
+    const Row r = row_of(set, top);
+    if (!cut_k && !cut_p) cut.sure_end = kBins, cut.lo = kBins, cut.hi = -1, cut.bin_k = -1;
+    const int tiles = (p.V + kTile - 1) / kTile;
     if (tid == 0) s_count = 0u;
+    for (int i = tid; i < tiles; i += kThreads) s_sum[i] = 0ull;
     __syncthreads();
-    unsigned long long mine = 0;
-    for (int e = begin + tid * 4; e < end; e += kThreads * 4) {
-        const f32x4 l = logits4<F32, VEC>(row, e, end);
+    for (int e0 = begin; e0 < end; e0 += kTile) {
+        const int e = e0 + tid * 4;
+        const f32x4 l = ahead;
+        ahead = logits4<F32, VEC>(row, e + kTile, end);
+        unsigned long long mine = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (e + j >= end) break;
             const int bin = bin_of(l[j], r);
             if (bin == kBins - 1) continue;
             if (bin < cut.sure_end) {
-                mine += drawn_weight(l[j], r);
-            } else if (inside(bin)) {
+                mine += drawn_weight<true>(l[j], bin, r);
+            } else if (inside(bin, cut)) {
                 const unsigned at = atomicAdd(&s_count, 1u);
-                if (at < kList) s_place[at] = place_of(l[j], e + j);
+                if (at < kInside) s_inside.place[at] = place_of(l[j], e + j);
             }
         }
-    }
-    mine = block_sum(mine, s);
-    if (tid == 0) {
-        put(p.sums + (int64_t)b * kMaxChunks + c, mine);
-        s_base = s_count ? __hip_atomic_fetch_add(p.listed + b, s_count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+        if (__any(mine != 0ull)) {
+            mine = wave_sum(mine);
+            if (lane == 0) atomicAdd(&s_sum[e0 / kTile], mine);
+        }
     }
     __syncthreads();
-    for (unsigned i = tid; i < min(s_count, (unsigned)kList); i += kThreads)
-        if (s_base + i < kList) put(p.list + (int64_t)b * kList + s_base + i, s_place[i]);
-    if (!last_to_arrive(p.arrive + gridDim.y + b, p.chunks, &s_last)) return;
+    if (tid < (end - begin + kTile - 1) / kTile)
+        put(p.sums + (int64_t)b * kMaxTiles + begin / kTile + tid, s_sum[begin / kTile + tid]);
+    if (tid == 0)
+        s_base = s_count ? __hip_atomic_fetch_add(p.arrive + 3 * gridDim.y + b, s_count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+    __syncthreads();
+    for (unsigned i = tid; i < min(s_count, (unsigned)kInside); i += kThreads)
+        if (s_base + i < kInside) put(p.list + (int64_t)b * kListed + s_base + i, s_inside.place[i]);
+    if (!last_to_arrive(p.arrive + 2 * gridDim.y + b, p.chunks, &s_last)) return;
 
+    // sums, list length and list together: what the list holds past its length is not used
+    for (int i = tid; i < tiles; i += kThreads) s_sum[i] = get(p.sums + (int64_t)b * kMaxTiles + i);
+    unsigned long long place[kInside / kThreads];
+#pragma unroll
+    for (int i = 0; i < kInside / kThreads; ++i) place[i] = get(p.list + (int64_t)b * kListed + i * kThreads + tid);
     // The cut: the last place that is kept.  ~0: all of them, as without cuts.
     unsigned long long last_place = ~0ull;
-    const unsigned listed = get(p.listed + b);
+    const unsigned listed = get(p.arrive + 3 * gridDim.y + b);
+    __syncthreads();  // every thread has read the list's length
+    if (tid == 0) put(p.arrive + 3 * gridDim.y + b, 0u);
     const double pp = (double)fmaxf(top_p, 0.f);
     if (cut.bin_k >= 0 || cut.hi >= 0) {
-        if (listed <= kList) {
-            for (unsigned i = tid; i < listed; i += kThreads) {
-                const unsigned long long at = get(p.list + (int64_t)b * kList + i);
-                const int bin = bin_of(logit_of(at), r);
-                s_place[i] = at;
-                s_wt[i] = fixed(weight_of(logit_of(at), r));
-                s_in[i] = (bin == cut.bin_k ? 1 : 0) | (bin >= cut.lo && bin <= cut.hi ? 2 : 0);
-            }
-            __syncthreads();
-            constexpr int kPer = kList / kThreads;
-            unsigned rank_k[kPer] = {};
-            unsigned long long before_p[kPer] = {}, w1 = 0;
-            bool in_k[kPer] = {}, in_p[kPer] = {};
-            // ranks and sums before each listed token, by comparing it with every other one
+        if (listed <= kInside) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const unsigned me = tid + i * kThreads;
-                if (me >= listed) continue;
-                const unsigned long long at = s_place[me];
-                in_k[i] = s_in[me] & 1;
-                in_p[i] = s_in[me] & 2;
-                for (unsigned o = 0; o < listed; ++o) {
-                    const bool earlier = s_place[o] < at;
-                    rank_k[i] += earlier && (s_in[o] & 1);
-                    before_p[i] += earlier && (s_in[o] & 2) ? s_wt[o] : 0ull;
-                }
-                if (in_k[i] && rank_k[i] < cut.left_k) w1 += s_wt[me];
-            }
-            w1 = block_sum(w1, s);
-            const double want = pp * (double)(cut.bin_k >= 0 ? cut.sum_before_k + w1 : cut.sum_all);
-            unsigned long long kept = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const unsigned me = tid + i * kThreads;
-                if (me >= listed) continue;
-                bool keep = true;
-                if (cut.bin_k >= 0 && in_k[i]) keep = rank_k[i] < cut.left_k;
-                if (cut_p) {
-                    const unsigned long long before = cut.sum_before_lo + before_p[i];
-                    keep = keep && in_p[i] && ((double)before < want || s_place[me] == best);
-                }
-                if (keep && s_place[me] > kept) kept = s_place[me];
-            }
-            last_place = ~block_min(~kept, s);
+            for (unsigned n = 0; n < kInside / kThreads; ++n)
+                if (n * kThreads + tid < listed) put_inside(s_inside, n * kThreads + tid, place[n], cut, r);
+            last_place = cut_of(s_inside, listed, cut, top_p, best, s);
         } else {
             // More tokens in the cuts' bins than the list holds (thousands of equal or nearly
             // equal logits): halve the range of places until the cut is found, each step one
@@ -552,7 +1007,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
             auto count_and_sum = [&](unsigned long long upto, int from, int to, unsigned long long *n_out,
                                      unsigned long long *w_out) {
                 unsigned long long n = 0, w = 0;
-                for (int e = tid * 4; e < p.V; e += kThreads * 4) {
+                for (int e = tid * 4; e < p.V; e += kTile) {
                     const f32x4 l = logits4<F32, VEC>(row, e, p.V);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -560,14 +1015,14 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
                         const int bin = bin_of(l[j], r);
                         if (bin < from || bin > to || bin == kBins - 1) continue;
                         ++n;
-                        w += fixed(weight_of(l[j], r));
+                        w += fixed_weight(l[j], bin, r);
                     }
                 }
                 *n_out = block_sum(n, s);
                 *w_out = block_sum(w, s);
             };
             unsigned long long n, w, lo, hi, kept = ~0ull;
-            double all = (double)cut.sum_all;
+            double all = cut.sum_all;
             if (cut.bin_k >= 0) {
                 // the smallest place with at least left_k tokens of bin_k up to it
                 lo = best, hi = ~0ull;
@@ -601,77 +1056,37 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
         }
     }
 
-    // Kept weights of the cuts' bins join their chunks' sums.
-    __shared__ unsigned long long s_sum[kMaxChunks];
-    __syncthreads();
-    if (tid < p.chunks) s_sum[tid] = get(p.sums + (int64_t)b * kMaxChunks + tid);
+    // Kept weights of the cuts' bins join their tiles' sums.
     __syncthreads();
     const bool cuts = cut.bin_k >= 0 || cut.hi >= 0;
-    if (cuts && listed <= kList) {
+    if (cuts && listed <= kInside) {
         for (unsigned i = tid; i < listed; i += kThreads)
-            if (s_place[i] <= last_place)
-                atomicAdd(&s_sum[(uint32_t)s_place[i] / (unsigned)p.chunk_len], drawn_weight(logit_of(s_place[i]), r));
+            if (s_inside.place[i] <= last_place) {
+                const float l = logit_of(s_inside.place[i]);
+                atomicAdd(&s_sum[(uint32_t)s_inside.place[i] / kTile], drawn_weight(l, bin_of(l, r), r));
+            }
     } else if (cuts) {
-        for (int e = tid; e < p.V; e += kThreads) {
-            const float l = logit_at<F32>(row, e);
-            const int bin = bin_of(l, r);
-            if (bin != kBins - 1 && bin >= cut.sure_end && place_of(l, e) <= last_place)
-                atomicAdd(&s_sum[e / p.chunk_len], drawn_weight(l, r));
+        for (int e0 = 0; e0 < p.V; e0 += kTile) {
+            const f32x4 l = logits4<F32, VEC>(row, e0 + tid * 4, p.V);
+            unsigned long long w = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int bin = bin_of(l[j], r);
+                if (bin != kBins - 1 && bin >= cut.sure_end && place_of(l[j], e0 + tid * 4 + j) <= last_place)
+                    w += drawn_weight(l[j], bin, r);
+            }
+            w = wave_sum(w);
+            if (lane == 0 && w) atomicAdd(&s_sum[e0 / kTile], w);
         }
     }
-    __syncthreads();
-    // The chunk in which the running sum passes the target, then the wave's segment of that
-    // chunk, then the token.  A target that rounding or u >= 1 puts past the end takes the last
-    // token that weighs anything.
-    unsigned long long total = 0;
-    for (int i = 0; i < p.chunks; ++i) total += s_sum[i];
-    const double u = (double)p.u[b];
-    const double real = u > 0.0 ? u * (double)total : 0.0;
-    unsigned long long target = real < (double)total ? (unsigned long long)real : total;
-    if (target >= total) target = total - 1;  // drawn where the running sum first exceeds target
-    int pick = 0;
-    while (pick < p.chunks - 1 && target >= s_sum[pick]) target -= s_sum[pick++];
-    const int cb = pick * p.chunk_len, ce = min(p.V, cb + p.chunk_len);
-    const int seg = ((ce - cb + kWaves - 1) / kWaves + 63) / 64 * 64;
-    const int sb = min(ce, cb + wave * seg), se = min(ce, sb + seg);
-    auto kept_weight = [&](int e) -> unsigned long long {
-        if (e >= se) return 0ull;
-        const float l = logit_at<F32>(row, e);
-        const int bin = bin_of(l, r);
-        if (bin == kBins - 1 || (bin >= cut.sure_end && place_of(l, e) > last_place)) return 0ull;
-        return drawn_weight(l, r);
-    };
-    unsigned long long part = 0;
-    for (int e = sb + lane; e < se; e += 64) part += kept_weight(e);
-    part = wave_sum(part);
-    __syncthreads();
-    if (lane == 0) s[wave] = part;
-    __syncthreads();
-    unsigned long long before = 0;
-    for (int i = 0; i < wave; ++i) before += s[i];
-    if (target < before || target >= before + part) return;  // another wave's segment
-    target -= before;
-    for (int e = sb; e < se; e += 64) {
-        const unsigned long long w = kept_weight(e + lane);
-        const unsigned long long run = wave_scan(w, lane);
-        const unsigned long long whole = __shfl(run, 63, 64);
-        if (target >= whole) {
-            target -= whole;
-            continue;
-        }
-        if (run > target && run - w <= target) {
-            p.token[b] = e + lane;
-            if (p.prob) p.prob[b] = (float)(weight_of(logit_at<F32>(row, e + lane), r) * kUnit / (double)total);
-        }
-        return;
-    }
+    draw_token<F32, VEC>(p, b, row, r, set.u, cut.sure_end, last_place, s_sum, tiles, s);
 }
 
 template <bool F32, bool VEC>
 void launch_sample(const SampleParams &p, int64_t B, bool cuts, hipStream_t stream)
 {
     const dim3 grid((unsigned)p.chunks, (unsigned)B), block(kThreads);
-    hipLaunchKernelGGL((sample_top_kernel<F32, VEC>), grid, block, 0, stream, p, cuts);
+    hipLaunchKernelGGL((sample_list_kernel<F32, VEC>), grid, block, 0, stream, p);
     if (cuts) hipLaunchKernelGGL((sample_bins_kernel<F32, VEC>), grid, block, 0, stream, p);
     hipLaunchKernelGGL((sample_draw_kernel<F32, VEC>), grid, block, 0, stream, p);
 }
@@ -708,29 +1123,31 @@ w4_status w4_sample(const void *logits, int logits_type, int64_t row_stride, con
     w4_status st = check_device(&dev);
     if (st != W4_OK) return st;
     const int64_t rows = B < kRows ? B : kRows;
-    // about two workgroups a CU, and chunks of 4096 logits or more
-    int64_t chunks = 512 / rows;
-    if (chunks > V / 4096) chunks = V / 4096;
-    if (chunks < 1) chunks = 1;
-    if (chunks > kMaxChunks) chunks = kMaxChunks;
-    const size_t words = (size_t)2 * kMaxChunks + kBins + kList;  // 8-byte words a row
+    // about five workgroups a CU
+    const int64_t most = (V + kMinChunk - 1) / kMinChunk, least = (V + kMaxChunk - 1) / kMaxChunk;
+    int64_t chunks = 1280 / rows < most ? 1280 / rows : most;
+    if (chunks < least) chunks = least;
+    const int64_t chunk = ((V + chunks - 1) / chunks + kTile - 1) / kTile * kTile;
+    const size_t words = (size_t)3 * kMaxChunks + 2 * kMaxTiles + kBins + kListed;  // 8-byte words a row
     unsigned *count = nullptr;
     float *part = nullptr;
-    st = get_workspace(dev, (hipStream_t)stream, (size_t)2 * rows,
-                       (size_t)rows * (words * 8 + sizeof(RowCut) + (kBins + 1) * 4), &count, &part);
+    st = get_workspace(dev, (hipStream_t)stream, (size_t)4 * rows,
+                       (size_t)rows * (words * 8 + sizeof(RowCut) + kBins * 4), &count, &part);
     if (st != W4_OK) return st;
     SampleParams p;
     p.stride = row_stride, p.V = (int)V;
-    p.chunk_len = (int)(((V + chunks - 1) / chunks + 3) / 4 * 4);
+    p.chunk_len = (int)chunk;
     p.chunks = (int)((V + p.chunk_len - 1) / p.chunk_len);
     p.arrive = count;
     p.top = (unsigned long long *)part;
-    p.sums = p.top + rows * kMaxChunks;
-    p.hist_w = p.sums + rows * kMaxChunks;
+    p.bound = (float *)(p.top + rows * kMaxChunks);
+    p.count = (unsigned *)(p.bound + rows * kMaxChunks * 2);
+    p.tile_sum = (double *)(p.count + rows * kMaxChunks * 2);
+    p.sums = (unsigned long long *)(p.tile_sum + rows * kMaxTiles);
+    p.hist_w = p.sums + rows * kMaxTiles;
     p.list = p.hist_w + rows * kBins;
-    p.cut = (RowCut *)(p.list + rows * kList);
+    p.cut = (RowCut *)(p.list + rows * kListed);
     p.hist_n = (unsigned *)(p.cut + rows);
-    p.listed = p.hist_n + rows * kBins;
     const bool vec = aligned(logits, 16) && row_stride * size % 16 == 0;
     const bool cuts = top_k || top_p;
     for (int64_t b = 0; b < B; b += kRows) {
