@@ -165,17 +165,16 @@ def plan(M: int, K: int, N: int, bits: int = 4, a4: bool = False) -> Dict[str, i
 
 
 def _stream_handle(stream) -> int:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us of a call's 13)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
 def _check(t, name, dtype, ndim):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
@@ -358,7 +357,7 @@ def _typed(t, name, ndim) -> int:
     """Type number of a device tensor of float32 or bfloat16 whose innermost dimension is contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     kind = _TYPES.get(t.dtype)
     if kind is None:
@@ -394,7 +393,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, bits: int = 16, residu
         if residual.shape != x.shape:
             raise ValueError("residual has another shape than x")
         if residual_out is None:
-            residual_out = torch.empty((M, H), dtype=residual.dtype, device=x.device)
+            residual_out = x.new_empty((M, H), dtype=residual.dtype)
         else:
             _check(residual_out, "residual_out", residual.dtype, 2)
             if residual_out.shape != x.shape:
@@ -404,11 +403,11 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, bits: int = 16, residu
         raise ValueError("residual_out needs a residual")
     scales, s_ptr = None, None
     if bits == 16:
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        y = x.new_empty((M, H), dtype=torch.bfloat16)
     elif bits == 8 or bits == 4:
-        y = torch.empty((M, H) if bits == 8 else (M, H // 8), dtype=torch.int8 if bits == 8 else torch.int32,
-                        device=x.device)
-        scales = torch.empty((M, H // 128), dtype=torch.float32, device=x.device)
+        y = (x.new_empty((M, H), dtype=torch.int8) if bits == 8 else
+             x.new_empty((M, H // 8), dtype=torch.int32))
+        scales = x.new_empty((M, H // 128), dtype=torch.float32)
         s_ptr = scales.data_ptr()
     else:
         raise ValueError("bits must be 16, 8 or 4")
@@ -438,7 +437,7 @@ def dequantize_activations(codes, scales, bits: int = 4, out=None, stream=None):
     if tuple(scales.shape) != (M, K // 128):
         raise ValueError(f"scales must be [{M}, {K // 128}]")
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float32, device=codes.device)
+        out = scales.new_empty((M, K))
     else:
         _check(out, "out", torch.float32, 2)
         if tuple(out.shape) != (M, K):
@@ -505,8 +504,8 @@ def kv_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=torch.bfl
         raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
     T = slots.shape[0]
     pages, heads, page_size, D = k_cache.shape
-    k = torch.empty((T, heads, D), dtype=dtype, device=k_cache.device)
-    v = torch.empty((T, heads, D), dtype=dtype, device=k_cache.device)
+    k = k_cache.new_empty((T, heads, D), dtype=dtype)
+    v = k_cache.new_empty((T, heads, D), dtype=dtype)
     rc = _lib.w4_kv_read(slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bits, k.data_ptr(),
                          v.data_ptr(), _TYPES[dtype], T, heads, D, pages, page_size, _stream_handle(stream))
     if rc:
@@ -532,7 +531,7 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, kv_len, max_q: in
     pages, kv_heads, page_size, cache_d = k_cache.shape
     if block_table.dtype != torch.int32:
         raise TypeError("block_table must be int32")
-    if block_table.device.type != "cuda" or block_table.dim() != 2 or (block_table.shape[1] > 1
+    if not block_table.is_cuda or block_table.dim() != 2 or (block_table.shape[1] > 1
                                                                        and block_table.stride(1) != 1):
         raise ValueError("block_table must be a 2-d device tensor with a contiguous last dimension")
     B, width = block_table.shape
@@ -543,7 +542,7 @@ def paged_attention(q, k_cache, v_cache, block_table, q_start, kv_len, max_q: in
                          f"block_table{tuple(block_table.shape)} q_start{tuple(q_start.shape)} "
                          f"kv_len{tuple(kv_len.shape)}")
     if out is None:
-        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((T, heads, D))
     else:
         _check(out, "out", torch.bfloat16, 3)
         if out.shape != q.shape:
@@ -579,8 +578,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stre
         if t.shape[0] != B:
             raise ValueError(f"{name} must be [{B}]")
         ptrs.append(t.data_ptr())
-    token = torch.empty(B, dtype=torch.int32, device=logits.device)
-    prob = torch.empty(B, dtype=torch.float32, device=logits.device)
+    token = u.new_empty(B, dtype=torch.int32)
+    prob = u.new_empty(B)
     rc = _lib.w4_sample(logits.data_ptr(), kind, _row_stride(logits), *ptrs, token.data_ptr(), prob.data_ptr(), B, V,
                         _stream_handle(stream))
     if rc:

@@ -21,8 +21,15 @@ using namespace w4dev;
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kBlock = 32;        // tokens of one step
+constexpr int kBlock = 32;        // tokens of one step of a wave (few rows)
+constexpr int kRowsGrain = 4 * kBlock;
+constexpr int kTile = 64;         // tokens of one step of a workgroup (many rows)
+#ifndef W4_TILES_RT
+#define W4_TILES_RT 1
+#endif
+constexpr int kMaxSplits = 64;
 constexpr float kLag = 8.0f;      // log2 by which a running maximum may lag
 constexpr float kNone = -__builtin_huge_valf();
 
@@ -57,16 +64,18 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int b)
     return s;
 }
 
-// How a row block's `blocks` steps are shared out: `per` for each split but the last used one.
+// How a row block's tokens are shared out over splits, in grains: `per` tokens for each used split
+// but the last.
 struct Share {
     int per, used;
 };
-__device__ __forceinline__ Share share_of(int tokens, int splits, int waves)
+__device__ __forceinline__ Share share_of(int tokens, int splits, int grain)
 {
-    const int blocks = (tokens + kBlock - 1) / kBlock;
+    const int grains = (tokens + grain - 1) / grain;
     Share s;
-    s.per = max(1, ((blocks + splits - 1) / splits + waves - 1) / waves * waves);
-    s.used = max(1, (blocks + s.per - 1) / s.per);
+    s.per = max(1, (grains + splits - 1) / splits);
+    s.used = max(1, (grains + s.per - 1) / s.per);
+    s.per *= grain;
     return s;
 }
 
@@ -76,9 +85,54 @@ __device__ __forceinline__ int tokens_of(const Seq &s, int last_row, int G)
     return max(0, s.kv - s.n + last_row / G + 1);
 }
 
+// Page lookups run a step ahead of the loads that need them, one 16-token tile (which lies in one
+// page) a lane: the page number is loaded when the step before is, and made a place when it is
+// needed, in scalar registers.
+__device__ __forceinline__ int page_of(const AttnParams &p, int tile)
+{
+    return (int)((uint64_t)(uint32_t)tile * p.page_magic >> 32);
+}
+__device__ __forceinline__ int page_number(const AttnParams &p, int b, int tile)
+{
+    const int page = page_of(p, tile);
+    return page < p.width ? p.table[(int64_t)b * p.table_stride + page] : -1;
+}
+// Row index of a tile's first token in the cache, or -1 for a bad page number.
+__device__ __forceinline__ int64_t tile_row(const AttnParams &p, int h, int tile, int id)
+{
+    if (id < 0 || id >= p.pages) return -1;
+    return ((int64_t)id * p.Hkv + h) * (p.page_tiles * 16) + (tile - page_of(p, tile) * p.page_tiles) * 16;
+}
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane)
+{
+    return (int64_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// Infinite or NaN values among tokens that some row of the block does not see: a weight of 0 does
+// not take them away, so they are cleared on the way in, their tokens noted (a bit each, from the
+// first such token's step on), and added to the rows that see them at the end.
+constexpr int kWildWords = 32;
+__device__ __forceinline__ uint32_t clear_wild(uint32_t x, bool &odd)
+{
+    const bool lo = (x & 0x7F80u) == 0x7F80u, hi = (x & 0x7F800000u) == 0x7F800000u;
+    odd = odd || lo || hi;
+    return (lo ? 0u : x & 0xFFFFu) | (hi ? 0u : x & 0xFFFF0000u);
+}
+__device__ __forceinline__ float wild_part(uint32_t bits16)  // the value if it is infinite or NaN, else 0
+{
+    return (bits16 & 0x7F80u) == 0x7F80u ? __builtin_bit_cast(float, bits16 << 16) : 0.f;
+}
+
 __device__ __forceinline__ f32x4 mfma16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+__device__ __forceinline__ f32x16 mfma32(const u32x4 &a, const u32x4 &b, const f32x16 &c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
 }
 
@@ -119,6 +173,7 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
     constexpr int kRowPad = D + 4;
     __shared__ __align__(16) float s_o[4][16 * kRowPad];
     __shared__ float s_m[4][16 * RT], s_l[4][16 * RT];
+    __shared__ uint32_t s_wild[kWildWords];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, quad = lane >> 4;
     const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits, h = blockIdx.y, b = blockIdx.z;
@@ -127,10 +182,9 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
     if (r0 >= rows) return;
     const int last = min(rows, r0 + 16 * RT) - 1;
     const int tokens = tokens_of(sq, last, p.G);
-    const Share sh = share_of(tokens, p.splits, 4);
+    const Share sh = share_of(tokens, p.splits, kRowsGrain);
     if (split >= sh.used) return;
-    const int blocks = (tokens + kBlock - 1) / kBlock;
-    const int blk_end = min(blocks, (split + 1) * sh.per);
+    const int blk_end = (min(tokens, (split + 1) * sh.per) + kBlock - 1) / kBlock;
     const int first_pos = sq.kv - sq.n + r0 / p.G;   // the least position of the rows
 
     // queries: row c of each row tile, the columns of operand B's step
@@ -166,19 +220,14 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         l[rt] = 0.f;
     }
 
-    // The place of a 16-token tile: row index of its first token in the cache, or -1.
-    auto tile_row = [&](int tile) -> int64_t {
-        const int page = (int)((uint64_t)(uint32_t)tile * p.page_magic >> 32);
-        int id = -1;
-        if (page < p.width) id = p.table[(int64_t)b * p.table_stride + page];
-        if (id < 0 || id >= p.pages) return -1;
-        return ((int64_t)id * p.Hkv + h) * (p.page_tiles * 16) + (tile - page * p.page_tiles) * 16;
-    };
     const int last_tile = (tokens - 1) / 16;
-    auto rows_of = [&](int blk, int64_t (&row)[2]) {
-        row[0] = tile_row(min(2 * blk, last_tile));
-        row[1] = tile_row(min(2 * blk + 1, last_tile));
+    auto number = [&](int blk) { return page_number(p, b, min(2 * blk + (lane & 1), last_tile)); };
+    auto rows_of = [&](int blk, int id, int64_t (&row)[2]) {
+        const int64_t at = tile_row(p, h, min(2 * blk + (lane & 1), last_tile), id);
+        row[0] = lane_value(at, 0);
+        row[1] = lane_value(at, 1);
     };
+    const int wild_from = max(first_pos, 0) / kBlock * kBlock;  // no step before it has a token that a row does not see
     auto load_k = [&](const int64_t (&row)[2], KeyRegs<D, I8> &kr) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -290,65 +339,20 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 #pragma unroll
             for (int e = 0; e < 4; ++e) pf[rt][e] = pack_bf16(w[2 * e], w[2 * e + 1]);
         }
-        bool wild = false;
         if constexpr (!I8) {
             if (masked || bad0 || bad1) {
                 // What lies behind the sequence's end in its last page, and what a bad page number
-                // stands for, may be anything: cleared.  A value that some row does not see may
-                // be infinite or NaN, which a weight of 0 does not take away: set aside.
-                uint32_t odd = 0;
+                // stands for, may be anything.
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const bool none = (e < 4 ? bad0 : bad1) || t0 + 16 * (e >> 2) + 4 * quad + (e & 3) >= sq.kv;
+                    const int tok = t0 + 16 * (e >> 2) + 4 * quad + (e & 3);
+                    const bool none = (e < 4 ? bad0 : bad1) || tok >= sq.kv;
+                    bool odd = false;
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        if (none) vr.v[e][j] = 0u;
-                        odd |= (vr.v[e][j] & 0x7F80u) == 0x7F80u;
-                        odd |= (vr.v[e][j] & 0x7F800000u) == 0x7F800000u;
-                    }
+                    for (int j = 0; j < D / 32; ++j)
+                        vr.v[e][j] = none ? 0u : masked ? clear_wild(vr.v[e][j], odd) : vr.v[e][j];
+                    if (odd) atomicOr(&s_wild[(tok - wild_from) / 32 % kWildWords], 1u << (tok - wild_from) % 32);
                 }
-                wild = __any(odd);
-            }
-        }
-        if constexpr (!I8) {
-            if (wild) {
-                // Each kind of such values by itself: which of them a row sees is a product of two
-                // 0/1 matrices, and a row that sees one gets it.
-                for (int kind = 0; kind < 3; ++kind) {
-                    auto is = [&](uint32_t x) -> uint32_t {  // 1.0 in bfloat16 where x is of this kind
-                        const bool y = kind == 0 ? (x & 0x7FFFu) > 0x7F80u : x == (kind == 1 ? 0x7F80u : 0xFF80u);
-                        return y ? 0x3F80u : 0u;
-                    };
-                    const float value = kind == 0 ? __builtin_nanf("") : kind == 1 ? -kNone : kNone;
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        u32x4 seen;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = t0 + 16 * (e >> 1) + 4 * quad + 2 * (e & 1);
-                            seen[e] = (tok <= pos[rt] ? 0x3F80u : 0u) | (tok + 1 <= pos[rt] ? 0x3F800000u : 0u);
-                        }
-#pragma unroll
-                        for (int j = 0; j < kCols; ++j) {
-                            u32x4 a;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                a[e] = is((vr.v[2 * e][j >> 1] >> (16 * (j & 1))) & 0xFFFFu) |
-                                       is((vr.v[2 * e + 1][j >> 1] >> (16 * (j & 1))) & 0xFFFFu) << 16;
-                            const f32x4 n = mfma16(a, seen, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (n[i] > 0.f) acc[rt][j][i] += value;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        if ((vr.v[e][j] & 0x7F80u) == 0x7F80u) vr.v[e][j] &= 0xFFFF0000u;
-                        if ((vr.v[e][j] & 0x7F800000u) == 0x7F800000u) vr.v[e][j] &= 0xFFFFu;
-                    }
             }
         }
 #pragma unroll
@@ -367,17 +371,22 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         }
     };
 
-    int blk = split * sh.per + wave;
+    if (threadIdx.x < kWildWords) s_wild[threadIdx.x] = 0u;
+    __syncthreads();
+    int blk = split * (sh.per / kBlock) + wave;
     if (blk < blk_end) {
         KeyRegs<D, I8> kr;
         ValueRegs<D, I8> vr;
         int64_t row[2], next[2];
-        rows_of(blk, row);
+        rows_of(blk, number(blk), row);
+        int id = number(min(blk + 4, blk_end - 1));
         load_k(row, kr);
         for (; blk < blk_end; blk += 4) {
             load_v(row, vr);
             KeyRegs<D, I8> kn;
-            rows_of(min(blk + 4, blk_end - 1), next);
+            const int ahead = min(blk + 4, blk_end - 1);
+            rows_of(ahead, id, next);
+            id = number(min(blk + 8, blk_end - 1));
             load_k(next, kn);
             step(blk, row, kr, vr);
             kr = kn;
@@ -420,6 +429,18 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 #pragma unroll
                 for (int w = 1; w < 4; ++w) o[j] += s_o[w][row * kRowPad + col + j];
             }
+            if constexpr (!I8) {
+                // the rows of a block lie within 64 positions, and this split's steps may end before
+                for (int word = 0; word < kWildWords; ++word)
+                    for (uint32_t bits = s_wild[word]; bits; bits &= bits - 1) {
+                        const int tok = wild_from + 32 * word + __builtin_ctz(bits);
+                        if (tok > sq.kv - sq.n + r / p.G) continue;
+                        const int64_t at = tile_row(p, h, tok / 16, page_number(p, b, tok / 16));
+                        const uint16_t *v = (const uint16_t *)p.v + (at + tok % 16) * D + col;
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) o[j] += wild_part(v[j]);
+                    }
+            }
             float M = s_m[0][16 * rt + row], L = 0.f;
 #pragma unroll
             for (int w = 1; w < 4; ++w) M = fmaxf(M, s_m[w][16 * rt + row]);
@@ -452,61 +473,459 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
     }
 }
 
-// Joins the splits of a row, in split order: one wave a row, D / 64 columns a lane.
-template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int block_rows, int waves)
+// ------------------------------------------------------------------------------------
+// Many rows: tiles of 64 tokens through LDS.
+//
+// A workgroup of 4 waves takes 128 * RT rows of one key/value head, 32 * RT a wave, and walks the
+// tokens 64 at a time, the next tile's loads in flight while one is computed (two LDS buffers, one
+// barrier a tile).
+//   S^T = K Q^T on 32x32x16: lane l gets, for row l % 32, the tokens 8 g + 4 (l / 32) + 0..3 of each
+//     32.  K lies in LDS as it comes, rows padded by 16 bytes.
+//   O^T = V^T P^T: the weights are operand B as they are, if operand A's k slots are the same
+//     tokens.  V lies in LDS transposed, each column's tokens in that order, so operand A is one
+//     16-byte read.  The transpose is done on the way in: a thread loads 8 columns of 4 tokens and
+//     puts pairs of tokens together with one byte permute each.  A column's 16-byte units are
+//     XORed with (column ^ column / 8) % 8: no bank conflicts on either side.
+template <int D, bool I8, int RT>
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const AttnParams p)
 {
-    constexpr int kPer = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int b = blockIdx.y;
+    constexpr int kSteps = D / 16;   // k-steps of the scores
+    constexpr int kCols = D / 32;    // output tiles
+    constexpr int kKeyRow = D * 2 + 16;
+    constexpr int kChunks = D / 8;   // 8-column chunks of a row
+    constexpr int kRows = 128 * RT;
+    __shared__ __align__(16) char s_k[2][kTile * kKeyRow];
+    __shared__ __align__(16) char s_v[2][D * kTile * 2];
+    __shared__ __align__(16) float s_ks[2][kTile], s_vs[2][kTile];
+    __shared__ uint32_t s_wild[kWildWords];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 31, half = lane >> 5;
+    const int split = blockIdx.x % p.splits, h = blockIdx.y, b = blockIdx.z;
+    const int rb = gridDim.x / p.splits - 1 - blockIdx.x / p.splits;  // the longest row blocks first
     const Seq sq = seq_of(p, b);
-    const int64_t x = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int i = (int)(x / p.Hq), hq = (int)(x - (int64_t)i * p.Hq);
+    const int rows = sq.n * p.G, r0 = rb * kRows;
+    if (r0 >= rows) return;
+    const int last = min(rows, r0 + kRows) - 1;
+    const int tokens = tokens_of(sq, last, p.G);
+    const Share sh = share_of(tokens, p.splits, kTile);
+    if (split >= sh.used) return;
+    const int t_begin = split * sh.per, t_end = min(tokens, t_begin + sh.per);
+    const int w0 = r0 + wave * 32 * RT;              // the wave's first row
+    const int first_pos = sq.kv - sq.n + min(w0, rows - 1) / p.G;
+    const int last_pos = sq.kv - sq.n + min(w0 + 32 * RT - 1, rows - 1) / p.G;
+    const int block_pos = sq.kv - sq.n + r0 / p.G;   // the least position of the workgroup's rows
+    const int wild_from = max(block_pos, 0) / kTile * kTile;  // no tile before it has a token that a row does not see
+
+    u32x4 qf[RT][kSteps];
+    int pos[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = min(w0 + 32 * rt + c, rows - 1);
+        const int i = r / p.G, g = r - i * p.G;
+        pos[rt] = sq.kv - sq.n + i;
+        const uint16_t *src = p.q + (int64_t)(sq.start + i) * p.q_tok_stride + (int64_t)(h * p.G + g) * p.q_head_stride;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            if (p.q_vec) {
+                qf[rt][s] = *(const u32x4 *)(src + d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    qf[rt][s][j] = (uint32_t)src[d + 2 * j] | (uint32_t)src[d + 2 * j + 1] << 16;
+            }
+        }
+    }
+    f32x16 acc[RT][kCols];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[rt][j][i] = 0.f;
+        m[rt] = kNone;
+        l[rt] = 0.f;
+    }
+
+    // Staging.  Keys: 16-byte pieces, 8 (16 bits) or 16 (8 bits) values.  Values: 4 tokens x 8 columns.
+    constexpr int kKeyPieces = I8 ? D / 16 : D / 8;               // pieces of a row
+    constexpr int kKeyLoads = kTile * kKeyPieces / 256;           // a thread's pieces
+    constexpr int kKeyRows = 256 / kKeyPieces;                    // rows of one round of pieces
+    constexpr int kValueThreads = kTile / 4 * kChunks;            // threads with values (256, or 128 for D = 64)
+    struct Staged {
+        u32x4 k[kKeyLoads];
+        uint32_t v[4][I8 ? 2 : 4];
+        float s;
+        int bad;
+    };
+    const int k_row = tid / kKeyPieces, k_piece = tid % kKeyPieces;
+    const int v_quad = tid / kChunks, v_chunk = tid % kChunks;
+    const int last_tile = (tokens - 1) / 16;
+    auto number = [&](int t0) { return page_number(p, b, min(t0 / 16 + (lane & 3), last_tile)); };
+    auto load = [&](int t0, int id, Staged &g) {
+        const int64_t place = tile_row(p, h, min(t0 / 16 + (lane & 3), last_tile), id);
+        int64_t at[4];
+        g.bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at[i] = lane_value(place, i);
+            if (at[i] < 0) {
+                g.bad |= 1 << i;
+                at[i] = 0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeyLoads; ++i) {
+            const int row = i * kKeyRows + k_row, sub = row / 16;  // a wave's rows lie in one sub-tile or two
+            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
+            g.k[i] = *(const u32x4 *)((const char *)p.k + ((from + row % 16) * D) * (I8 ? 1 : 2) + k_piece * 16);
+        }
+        if (kValueThreads == 256 || tid < kValueThreads) {
+            const int sub = v_quad / 4;
+            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const char *a = (const char *)p.v +
+                                ((from + v_quad % 4 * 4 + e) * D + v_chunk * 8) * (I8 ? 1 : 2);
+                if constexpr (I8) {
+                    const u32x2 x = *(const u32x2 *)a;
+                    g.v[e][0] = x[0], g.v[e][1] = x[1];
+                } else {
+                    const u32x4 x = *(const u32x4 *)a;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g.v[e][j] = x[j];
+                }
+            }
+        }
+        if constexpr (I8) {
+            const int row = tid & 63, sub = row / 16;
+            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
+            if (wave < 2) g.s = (wave == 0 ? p.ks : p.vs)[from + row % 16];
+        }
+    };
+    auto store = [&](int t0, Staged &g, int buf) {
+#pragma unroll
+        for (int i = 0; i < kKeyLoads; ++i) {
+            char *dst = s_k[buf] + (i * kKeyRows + k_row) * kKeyRow;
+            if constexpr (I8) {
+                const u32x4 x = g.k[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *(u32x4 *)(dst + k_piece * 32 + 16 * j) =
+                        u32x4{pack_bf16(sbyte(x[2 * j], 0), sbyte(x[2 * j], 1)),
+                              pack_bf16(sbyte(x[2 * j], 2), sbyte(x[2 * j], 3)),
+                              pack_bf16(sbyte(x[2 * j + 1], 0), sbyte(x[2 * j + 1], 1)),
+                              pack_bf16(sbyte(x[2 * j + 1], 2), sbyte(x[2 * j + 1], 3))};
+            } else {
+                *(u32x4 *)(dst + k_piece * 16) = g.k[i];
+            }
+        }
+        if (kValueThreads == 256 || tid < kValueThreads) {
+            if constexpr (!I8) {
+                // What lies behind the sequence's end in its last page, and what a bad page number
+                // stands for, may be anything.
+                const bool masked = t0 + kTile - 1 > block_pos;  // then no token lies before wild_from
+                if (masked || g.bad) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = t0 + 4 * v_quad + e;
+                        const bool none = (g.bad >> (v_quad / 4) & 1) || tok >= sq.kv;
+                        bool odd = false;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            g.v[e][j] = none ? 0u : masked ? clear_wild(g.v[e][j], odd) : g.v[e][j];
+                        if (odd) atomicOr(&s_wild[(tok - wild_from) / 32 % kWildWords], 1u << (tok - wild_from) % 32);
+                    }
+                }
+            }
+            // token 16 s + 8 a + 4 h + e of a column goes to place 16 s + 8 h + 4 a + e
+            const int unit = 2 * (v_quad >> 2) + (v_quad & 1), a = v_quad >> 1 & 1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = v_chunk * 8 + j;
+                u32x2 x;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (I8)
+                        x[e] = pack_bf16(sbyte(g.v[2 * e][j >> 2], j & 3), sbyte(g.v[2 * e + 1][j >> 2], j & 3));
+                    else
+                        x[e] = __builtin_amdgcn_perm(g.v[2 * e + 1][j >> 1], g.v[2 * e][j >> 1],
+                                                     j & 1 ? 0x07060302u : 0x05040100u);
+                }
+                *(u32x2 *)(s_v[buf] + d * (kTile * 2) + ((unit ^ ((j ^ v_chunk) & 7)) * 16) + a * 8) = x;
+            }
+        }
+        if constexpr (I8) {
+            if (wave == 0) s_ks[buf][tid & 63] = g.s * p.scale2;
+            if (wave == 1) s_vs[buf][tid & 63] = g.s;
+        }
+    };
+
+    auto compute = [&](int t0, int buf, int bad) {
+        const bool masked = t0 + kTile - 1 > first_pos;
+        f32x16 sc[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[rt][t][i] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const u32x4 a = *(const u32x4 *)(s_k[buf] + (32 * t + c) * kKeyRow + 32 * s + 16 * half);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) sc[rt][t] = mfma32(a, qf[rt][s], sc[rt][t]);
+            }
+        u32x4 pf[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if constexpr (I8) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 f = *(const f32x4 *)(s_ks[buf] + 32 * t + 8 * g + 4 * half);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[rt][t][4 * g + e] *= f[e];
+                    }
+            }
+            if (bad) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (bad >> (2 * t + i / 8) & 1) sc[rt][t][i] = __builtin_nanf("");
+            }
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > pos[rt])
+                            sc[rt][t][i] = !I8 && p.scale2 < 0.f ? -kNone : kNone;
+            }
+            // the scores' maximum is the least of them under a negative scale
+            float mx = sc[rt][0][0];
+            if (!I8 && p.scale2 < 0.f) {
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx = fminf(mx, sc[rt][i >> 4][i & 15]);
+            } else {
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx = fmaxf(mx, sc[rt][i >> 4][i & 15]);
+            }
+            if constexpr (!I8) mx *= p.scale2;
+            if (__any(mx > m[rt] + kLag)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                mx = fmaxf(mx, m[rt]);
+                const float f = mx == kNone ? 1.f : exp2_fast(m[rt] - mx);
+                m[rt] = mx;
+                l[rt] *= f;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) acc[rt][j] *= f;
+            }
+            const float base = m[rt] == kNone ? 0.f : m[rt];
+            float w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float x = sc[rt][i >> 4][i & 15];
+                w[i] = exp2_fast(I8 ? x - base : __builtin_fmaf(x, p.scale2, -base));
+                l[rt] += w[i];
+            }
+            if constexpr (I8) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 f = *(const f32x4 *)(s_vs[buf] + 32 * t + 8 * g + 4 * half);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = w[16 * t + 4 * g + e] * f[e];
+                            // an unseen token's scale may be anything
+                            w[16 * t + 4 * g + e] = masked && sc[rt][t][4 * g + e] == kNone ? 0.f : y;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pf[rt][s][j] = pack_bf16(w[8 * s + 2 * j], w[8 * s + 2 * j + 1]);
+        }
+        auto value = [&](int j, int s) {
+            const int d = 32 * j + c;
+            return *(const u32x4 *)(s_v[buf] + d * (kTile * 2) + (((2 * s + half) ^ ((d ^ d >> 3) & 7)) * 16));
+        };
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const u32x4 a = value(j, s);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) acc[rt][j] = mfma32(a, pf[rt][s], acc[rt][j]);
+            }
+    };
+
+    if (tid < kWildWords) s_wild[tid] = 0u;
+    __syncthreads();
+    if (t_begin < t_end) {
+        Staged g;
+        load(t_begin, number(t_begin), g);
+        int id = number(t_begin + kTile);
+        int bad = g.bad, buf = 0;
+        store(t_begin, g, 0);
+        for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
+            __syncthreads();  // this tile is whole, the other buffer is free
+            const bool more = t0 + kTile < t_end;
+            if (more) {
+                load(t0 + kTile, id, g);
+                id = number(t0 + 2 * kTile);
+            }
+            if (t0 <= last_pos) compute(t0, buf, bad);  // else none of the wave's rows sees the tile
+            if (more) {
+                store(t0 + kTile, g, buf ^ 1);
+                bad = g.bad;
+            }
+            buf ^= 1;
+        }
+    }
+    if constexpr (!I8) {
+        __syncthreads();
+        for (int word = 0; word < kWildWords; ++word)
+            for (uint32_t bits = s_wild[word]; bits; bits &= bits - 1) {
+                const int tok = wild_from + 32 * word + __builtin_ctz(bits);
+                const int64_t at = tile_row(p, h, tok / 16, page_number(p, b, tok / 16)) + tok % 16;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = wild_part(((const uint16_t *)p.v)[at * D + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3)]);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            if (tok <= pos[rt]) acc[rt][j][i] += v;
+                    }
+            }
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = w0 + 32 * rt + c;
+        const float sum = l[rt] + __shfl_xor(l[rt], 32, 64);
+        if (r > last) continue;
+        const int i = r / p.G;
+        const int64_t at = (int64_t)(sq.start + i) * p.Hq + h * p.G + (r - i * p.G);
+        if (sh.used == 1) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *(u32x2 *)(p.out + at * D + 32 * j + 8 * g + 4 * half) =
+                        u32x2{pack_bf16(acc[rt][j][4 * g] * inv, acc[rt][j][4 * g + 1] * inv),
+                              pack_bf16(acc[rt][j][4 * g + 2] * inv, acc[rt][j][4 * g + 3] * inv)};
+        } else {
+            const int64_t pr = (int64_t)split * p.T * p.Hq + at;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *(f32x4 *)(p.part + pr * D + 32 * j + 8 * g + 4 * half) =
+                        f32x4{acc[rt][j][4 * g], acc[rt][j][4 * g + 1], acc[rt][j][4 * g + 2], acc[rt][j][4 * g + 3]};
+            if (half == 0) {
+                p.part_ml[pr * 2] = m[rt];
+                p.part_ml[pr * 2 + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the splits of a row, in split order within each of 8 shares: a workgroup a row, D / 4
+// lanes a split, all loads of a row in flight together.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int block_rows, int grain)
+{
+    constexpr int kLanes = D / 4, kShares = 256 / kLanes, kHeld = kMaxSplits / kShares;
+    __shared__ float s_f[kMaxSplits];
+    __shared__ float s_l[kMaxSplits];
+    __shared__ __align__(16) f32x4 s_o[kShares][kLanes];
+    const int tid = threadIdx.x, part = tid / kLanes, col = tid % kLanes;
+    const int b = blockIdx.y, i = blockIdx.x / p.Hq, hq = blockIdx.x - i * p.Hq;
+    const Seq sq = seq_of(p, b);
     if (i >= sq.n) return;
     const int r = i * p.G + hq % p.G;
     const int last = min(sq.n * p.G, (r / block_rows + 1) * block_rows) - 1;
-    const Share sh = share_of(tokens_of(sq, last, p.G), p.splits, waves);
+    const Share sh = share_of(tokens_of(sq, last, p.G), p.splits, grain);
     if (sh.used == 1) return;
     const int64_t at = (int64_t)(sq.start + i) * p.Hq + hq, stride = (int64_t)p.T * p.Hq;
-    float M = kNone, L = 0.f, o[kPer] = {};
-    for (int s = 0; s < sh.used; ++s) M = fmaxf(M, p.part_ml[(s * stride + at) * 2]);
-#pragma unroll 4
-    for (int s = 0; s < sh.used; ++s) {
-        const float *ml = p.part_ml + (s * stride + at) * 2;
-        const float f = ml[0] == kNone ? 1.f : exp2_fast(ml[0] - M);  // no maximum: zeros or NaN
-        L += ml[1] * f;
-        const float *src = p.part + (s * stride + at) * D + lane * kPer;
+    f32x4 x[kHeld];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] += src[j] * f;
+    for (int k = 0; k < kHeld; ++k) {
+        const int s = k * kShares + part;
+        if (s < sh.used) x[k] = *(const f32x4 *)(p.part + (s * stride + at) * D + col * 4);
     }
+    float m = kNone, l = 0.f;
+    if (tid < sh.used) {
+        m = p.part_ml[(tid * stride + at) * 2];
+        l = p.part_ml[(tid * stride + at) * 2 + 1];
+        s_f[tid] = m;
+    }
+    __syncthreads();
+    float M = kNone;
+    for (int s = 0; s < sh.used; ++s) M = fmaxf(M, s_f[s]);
+    __syncthreads();
+    if (tid < sh.used) {
+        const float f = m == kNone ? 1.f : exp2_fast(m - M);  // no maximum: zeros or NaN
+        s_f[tid] = f;
+        s_l[tid] = l * f;
+    }
+    __syncthreads();
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int s = k * kShares + part;
+        if (s < sh.used) o += x[k] * s_f[s];
+    }
+    s_o[part][col] = o;
+    __syncthreads();
+    if (tid >= kLanes) return;
+    float L = 0.f;
+    for (int s = 0; s < sh.used; ++s) L += s_l[s];
+#pragma unroll
+    for (int k = 1; k < kShares; ++k) o += s_o[k][col];
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    if constexpr (kPer == 2)
-        ((uint32_t *)(p.out + at * D))[lane] = pack_bf16(o[0] * inv, o[1] * inv);
-    else
-        ((__bf16 *)(p.out + at * D))[lane] = (__bf16)(o[0] * inv);
+    *(u32x2 *)(p.out + at * D + col * 4) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
-template <int D, bool I8, int RT>
-void launch_rows(const AttnParams &p, int64_t B, int64_t max_rows, hipStream_t stream)
-{
-    const dim3 grid((unsigned)((max_rows + 16 * RT - 1) / (16 * RT) * p.splits), (unsigned)p.Hkv, (unsigned)B);
-    hipLaunchKernelGGL((attn_rows_kernel<D, I8, RT>), grid, dim3(256), 0, stream, p);
-}
+// How a call is launched: rows of a workgroup, and which kernel takes them.
+struct Launch {
+    bool tiles;
+    int rt;          // row tiles of a wave (16 rows, or 32 with tiles)
+    int block_rows;  // rows of a workgroup
+    int grain;       // tokens that splits are multiples of
+};
 
 template <int D, bool I8>
-void launch_attention(const AttnParams &p, int64_t B, int64_t max_q, int rt, hipStream_t stream)
+void launch_attention(const AttnParams &p, const Launch &k, int64_t B, int64_t max_q, int64_t row_blocks,
+                      hipStream_t stream)
 {
-    const int64_t max_rows = max_q * p.G;
-    switch (rt) {
-    case 1: launch_rows<D, I8, 1>(p, B, max_rows, stream); break;
-    case 2: launch_rows<D, I8, 2>(p, B, max_rows, stream); break;
-    case 3: launch_rows<D, I8, 3>(p, B, max_rows, stream); break;
-    default: launch_rows<D, I8, 4>(p, B, max_rows, stream); break;
+    const dim3 grid((unsigned)(row_blocks * p.splits), (unsigned)p.Hkv, (unsigned)B), block(256);
+    if (k.tiles) {
+        if (k.rt == 1)
+            hipLaunchKernelGGL((attn_tiles_kernel<D, I8, 1>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((attn_tiles_kernel<D, I8, 2>), grid, block, 0, stream, p);
+    } else {
+        switch (k.rt) {
+        case 1: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 1>), grid, block, 0, stream, p); break;
+        case 2: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 2>), grid, block, 0, stream, p); break;
+        case 3: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 3>), grid, block, 0, stream, p); break;
+        default: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 4>), grid, block, 0, stream, p); break;
+        }
     }
-    if (p.splits > 1) {
-        const dim3 grid((unsigned)((max_q * p.Hq + 3) / 4), (unsigned)B);
-        hipLaunchKernelGGL(attn_join_kernel<D>, grid, dim3(256), 0, stream, p, 16 * rt, 4);
-    }
+    if (p.splits > 1)
+        hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(max_q * p.Hq), (unsigned)B), block, 0, stream, p,
+                           k.block_rows, k.grain);
 }
 
 }  // namespace
@@ -574,13 +993,19 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
     p.page_magic = (((uint64_t)1 << 32) + p.page_tiles - 1) / p.page_tiles;
     p.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     const int64_t max_rows = max_q * p.G;
-    const int rt = max_rows >= 64 ? 4 : (int)((max_rows + 15) / 16);
-    const int64_t row_blocks = (max_rows + 16 * rt - 1) / (16 * rt);
-    // enough workgroups to fill the card, each wave with one step or more
-    const int64_t units = row_blocks * kv_heads * B, steps = (max_kv + 4 * kBlock - 1) / (4 * kBlock);
-    int64_t splits = units >= 512 ? 1 : (512 + units - 1) / units;
+    Launch k;
+    k.tiles = max_rows > 64;
+    if (k.tiles)
+        k.rt = W4_TILES_RT, k.block_rows = 128 * k.rt, k.grain = kTile;
+    else
+        k.rt = (int)((max_rows + 15) / 16), k.block_rows = 16 * k.rt, k.grain = kRowsGrain;
+    const int64_t row_blocks = (max_rows + k.block_rows - 1) / k.block_rows;
+    // one round of workgroups over the card, each with a grain of tokens or more
+    const int64_t units = row_blocks * kv_heads * B, steps = (max_kv + k.grain - 1) / k.grain;
+    const int64_t room = (k.tiles ? k.rt == 1 : k.rt <= 2) ? 512 : 256;
+    int64_t splits = room / units;
     if (splits > steps) splits = steps;
-    if (splits > 128) splits = 128;
+    if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
     p.splits = (int)splits;
     p.part = p.part_ml = nullptr;
@@ -597,11 +1022,11 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
         return W4_ERR_SHAPE;
     }
     if (D == 128)
-        cache_bits == 8 ? launch_attention<128, true>(p, B, max_q, rt, (hipStream_t)stream)
-                        : launch_attention<128, false>(p, B, max_q, rt, (hipStream_t)stream);
+        cache_bits == 8 ? launch_attention<128, true>(p, k, B, max_q, row_blocks, (hipStream_t)stream)
+                        : launch_attention<128, false>(p, k, B, max_q, row_blocks, (hipStream_t)stream);
     else
-        cache_bits == 8 ? launch_attention<64, true>(p, B, max_q, rt, (hipStream_t)stream)
-                        : launch_attention<64, false>(p, B, max_q, rt, (hipStream_t)stream);
+        cache_bits == 8 ? launch_attention<64, true>(p, k, B, max_q, row_blocks, (hipStream_t)stream)
+                        : launch_attention<64, false>(p, k, B, max_q, row_blocks, (hipStream_t)stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return hip_fail("w4_paged_attention launch", e);
     return W4_OK;
