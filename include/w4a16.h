@@ -294,7 +294,7 @@ w4_status w4_kv_read(const int64_t *slots, const void *k_cache, const void *v_ca
  *   A page number outside [0, pages), or a token past the table's width, gives NaN in the rows
  *   that see such a token, and never an access outside the pool.
  *   What the caches hold past a sequence's end does not matter.
- *   page_size: a multiple of 16 up to 4096.  Scores, softmax and sums are float32; the weights
+ *   page_size: a multiple of 16 up to 4096; scale: finite.  Scores, softmax and sums are float32; the weights
  *   are rounded to bfloat16 for the matrix cores.  Bitwise reproducible.
  */
 w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,

@@ -26,9 +26,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kBlock = 32;        // tokens of one step of a wave (few rows)
 constexpr int kRowsGrain = 4 * kBlock;
 constexpr int kTile = 64;         // tokens of one step of a workgroup (many rows)
-#ifndef W4_TILES_RT
-#define W4_TILES_RT 1
-#endif
+constexpr int kTileRows = 128;    // rows of such a workgroup
 constexpr int kMaxSplits = 64;
 constexpr float kLag = 8.0f;      // log2 by which a running maximum may lag
 constexpr float kNone = -__builtin_huge_valf();
@@ -476,7 +474,7 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 // ------------------------------------------------------------------------------------
 // Many rows: tiles of 64 tokens through LDS.
 //
-// A workgroup of 4 waves takes 128 * RT rows of one key/value head, 32 * RT a wave, and walks the
+// A workgroup of 4 waves takes 128 rows of one key/value head, 32 a wave, and walks the
 // tokens 64 at a time, the next tile's loads in flight while one is computed (two LDS buffers, one
 // barrier a tile).
 //   S^T = K Q^T on 32x32x16: lane l gets, for row l % 32, the tokens 8 g + 4 (l / 32) + 0..3 of each
@@ -486,14 +484,15 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 //     16-byte read.  The transpose is done on the way in: a thread loads 8 columns of 4 tokens and
 //     puts pairs of tokens together with one byte permute each.  A column's 16-byte units are
 //     XORed with (column ^ column / 8) % 8: no bank conflicts on either side.
-template <int D, bool I8, int RT>
-__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const AttnParams p)
+template <int D, bool I8>
+__global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
 {
     constexpr int kSteps = D / 16;   // k-steps of the scores
     constexpr int kCols = D / 32;    // output tiles
     constexpr int kKeyRow = D * 2 + 16;
     constexpr int kChunks = D / 8;   // 8-column chunks of a row
-    constexpr int kRows = 128 * RT;
+    constexpr int kRowBytes = I8 ? D : 2 * D;
+    constexpr int kRows = kTileRows;
     __shared__ __align__(16) char s_k[2][kTile * kKeyRow];
     __shared__ __align__(16) char s_v[2][D * kTile * 2];
     __shared__ __align__(16) float s_ks[2][kTile], s_vs[2][kTile];
@@ -510,43 +509,35 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const 
     const Share sh = share_of(tokens, p.splits, kTile);
     if (split >= sh.used) return;
     const int t_begin = split * sh.per, t_end = min(tokens, t_begin + sh.per);
-    const int w0 = r0 + wave * 32 * RT;              // the wave's first row
-    const int first_pos = sq.kv - sq.n + min(w0, rows - 1) / p.G;
-    const int last_pos = sq.kv - sq.n + min(w0 + 32 * RT - 1, rows - 1) / p.G;
+    const int w0 = r0 + wave * 32;              // the wave's first row
+    const int last_pos = sq.kv - sq.n + min(w0 + 31, rows - 1) / p.G;
     const int block_pos = sq.kv - sq.n + r0 / p.G;   // the least position of the workgroup's rows
     const int wild_from = max(block_pos, 0) / kTile * kTile;  // no tile before it has a token that a row does not see
 
-    u32x4 qf[RT][kSteps];
-    int pos[RT];
+    u32x4 qf[kSteps];
+    const int r = min(w0 + c, rows - 1);             // the lane's row: token qi, head h * G + qg
+    const int qi = r / p.G, qg = r - qi * p.G, pos = sq.kv - sq.n + qi;
+    const uint16_t *src = p.q + (int64_t)(sq.start + qi) * p.q_tok_stride + (int64_t)(h * p.G + qg) * p.q_head_stride;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = min(w0 + 32 * rt + c, rows - 1);
-        const int i = r / p.G, g = r - i * p.G;
-        pos[rt] = sq.kv - sq.n + i;
-        const uint16_t *src = p.q + (int64_t)(sq.start + i) * p.q_tok_stride + (int64_t)(h * p.G + g) * p.q_head_stride;
+    for (int s = 0; s < kSteps; ++s) {
+        const int d = 16 * s + 8 * half;
+        if (p.q_vec) {
+            qf[s] = *(const u32x4 *)(src + d);
+        } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int d = 16 * s + 8 * half;
-            if (p.q_vec) {
-                qf[rt][s] = *(const u32x4 *)(src + d);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    qf[rt][s][j] = (uint32_t)src[d + 2 * j] | (uint32_t)src[d + 2 * j + 1] << 16;
-            }
+            for (int j = 0; j < 4; ++j)
+                qf[s][j] = (uint32_t)src[d + 2 * j] | (uint32_t)src[d + 2 * j + 1] << 16;
         }
+        // the scale's sign goes to the queries, so that the largest score is the largest product
+        if (p.scale2 < 0.f) qf[s] ^= 0x80008000u;
     }
-    f32x16 acc[RT][kCols];
-    float m[RT], l[RT];
+    const float scale2 = fmaxf(fabsf(p.scale2), 1e-30f);  // a scale of 0 must not make NaN of an unseen token's -infinity
+    f32x16 acc[kCols];
+    float m = kNone, l = 0.f;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+    for (int j = 0; j < kCols; ++j)
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[rt][j][i] = 0.f;
-        m[rt] = kNone;
-        l[rt] = 0.f;
-    }
+        for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
 
     // Staging.  Keys: 16-byte pieces, 8 (16 bits) or 16 (8 bits) values.  Values: 4 tokens x 8 columns.
     constexpr int kKeyPieces = I8 ? D / 16 : D / 8;               // pieces of a row
@@ -562,32 +553,44 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const 
     const int k_row = tid / kKeyPieces, k_piece = tid % kKeyPieces;
     const int v_quad = tid / kChunks, v_chunk = tid % kChunks;
     const int last_tile = (tokens - 1) / 16;
-    auto number = [&](int t0) { return page_number(p, b, min(t0 / 16 + (lane & 3), last_tile)); };
-    auto load = [&](int t0, int id, Staged &g) {
-        const int64_t place = tile_row(p, h, min(t0 / 16 + (lane & 3), last_tile), id);
-        int64_t at[4];
-        g.bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            at[i] = lane_value(place, i);
-            if (at[i] < 0) {
-                g.bad |= 1 << i;
-                at[i] = 0;
-            }
-        }
+    // Places of the next 64 sub-tiles of 16 tokens, one a lane, looked up every 16 tiles.
+    constexpr int kPlaces = 64 * 16;
+    auto number = [&](int from) __attribute__((always_inline)) {
+        return page_number(p, b, min(from / 16 + lane, last_tile));
+    };
+    int64_t places = 0;
+    uint64_t bad_places = 0;
+    auto look_up = [&](int from, int id) __attribute__((always_inline)) {
+        places = tile_row(p, h, min(from / 16 + lane, last_tile), id);
+        bad_places = __ballot(places < 0);
+        places = places < 0 ? 0 : places;
+    };
+    auto load = [&](int t0, Staged &g) __attribute__((always_inline)) {
+        const int first = (t0 - t_begin) % kPlaces / 16;   // the tile's first lane
+        g.bad = (int)(bad_places >> first) & 15;
+        // scalar bases where a wave reads one sub-tile, 32-bit lane offsets
+        auto base = [&](const void *pool, int sub) __attribute__((always_inline)) {
+            return (const char *)pool + lane_value(places, first + sub) * kRowBytes;
+        };
+        auto mixed = [&](int sub) __attribute__((always_inline)) {
+            return (int64_t)__shfl((long long)places, first + sub, 64);
+        };
 #pragma unroll
         for (int i = 0; i < kKeyLoads; ++i) {
-            const int row = i * kKeyRows + k_row, sub = row / 16;  // a wave's rows lie in one sub-tile or two
-            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
-            g.k[i] = *(const u32x4 *)((const char *)p.k + ((from + row % 16) * D) * (I8 ? 1 : 2) + k_piece * 16);
+            const uint32_t off = (uint32_t)(k_row % 16 * kRowBytes + k_piece * 16);
+            if constexpr (kKeyRows <= 16)  // a round of pieces lies in one sub-tile
+                g.k[i] = *(const u32x4 *)(base(p.k, i * kKeyRows / 16) + off);
+            else if constexpr (kKeyRows == 32)  // in one for each half of the waves
+                g.k[i] = *(const u32x4 *)(base(p.k, 2 * i + wave / 2) + off);
+            else  // in one for each wave
+                g.k[i] = *(const u32x4 *)(base(p.k, wave) + off);
         }
         if (kValueThreads == 256 || tid < kValueThreads) {
-            const int sub = v_quad / 4;
-            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
+            const uint32_t off = (uint32_t)(v_quad % 4 * 4 * kRowBytes + v_chunk * (I8 ? 8 : 16));
+            const char *from = D == 128 ? base(p.v, wave) + off : (const char *)p.v + mixed(v_quad / 4) * kRowBytes + off;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const char *a = (const char *)p.v +
-                                ((from + v_quad % 4 * 4 + e) * D + v_chunk * 8) * (I8 ? 1 : 2);
+                const char *a = from + e * kRowBytes;
                 if constexpr (I8) {
                     const u32x2 x = *(const u32x2 *)a;
                     g.v[e][0] = x[0], g.v[e][1] = x[1];
@@ -600,11 +603,11 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const 
         }
         if constexpr (I8) {
             const int row = tid & 63, sub = row / 16;
-            const int64_t from = sub < 2 ? (sub == 0 ? at[0] : at[1]) : (sub == 2 ? at[2] : at[3]);
+            const int64_t from = mixed(sub);
             if (wave < 2) g.s = (wave == 0 ? p.ks : p.vs)[from + row % 16];
         }
     };
-    auto store = [&](int t0, Staged &g, int buf) {
+    auto store = [&](int t0, Staged &g, int buf) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kKeyLoads; ++i) {
             char *dst = s_k[buf] + (i * kKeyRows + k_row) * kKeyRow;
@@ -657,138 +660,140 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const 
             }
         }
         if constexpr (I8) {
-            if (wave == 0) s_ks[buf][tid & 63] = g.s * p.scale2;
+            if (wave == 0) s_ks[buf][tid & 63] = g.s * scale2;
             if (wave == 1) s_vs[buf][tid & 63] = g.s;
         }
     };
 
-    auto compute = [&](int t0, int buf, int bad) {
-        const bool masked = t0 + kTile - 1 > first_pos;
-        f32x16 sc[RT][2];
+    // CARE: some row does not see some token, or a page number is bad.
+    auto compute = [&](int t0, int buf, int bad, auto care) __attribute__((always_inline)) {
+        constexpr bool CARE = decltype(care)::value;
+        // the keys' operands before the scores, the values' first ones before the softmax
+        u32x4 kf[2][kSteps];
+        const char *keys = s_k[buf] + c * kKeyRow + 16 * half;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) kf[t][s] = *(const u32x4 *)(keys + 32 * t * kKeyRow + 32 * s);
+        f32x16 sc[2];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sc[t] = mfma32(kf[t][s], qf[s], s ? sc[t] : f32x16{});
+        // column d = 32 j + c: its unit for step s is 2 s + half, XORed with (c ^ c / 8) % 8 and 4 (j % 2),
+        // which is that of step s ^ 2 at an even j
+        const char *values = s_v[buf] + c * (kTile * 2);
+        auto value = [&](int j, int s) __attribute__((always_inline)) {
+            const int step = j & 1 ? s ^ 2 : s;
+            return *(const u32x4 *)(values + 32 * j * (kTile * 2) + (((2 * step + half) ^ ((c ^ c >> 3) & 7)) * 16));
+        };
+        u32x4 vf[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) vf[j][s] = value(j, s);
+        u32x4 pf[4];
+        if constexpr (I8) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[rt][t][i] = 0.f;
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 f = *(const f32x4 *)(s_ks[buf] + 32 * t + 8 * g + 4 * half);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+                    for (int e = 0; e < 4; ++e) sc[t][4 * g + e] *= f[e];
+                }
+        }
+        if constexpr (CARE) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const u32x4 a = *(const u32x4 *)(s_k[buf] + (32 * t + c) * kKeyRow + 32 * s + 16 * half);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) sc[rt][t] = mfma32(a, qf[rt][s], sc[rt][t]);
-            }
-        u32x4 pf[RT][4];
+                for (int i = 0; i < 16; ++i) {
+                    if (bad >> (2 * t + i / 8) & 1) sc[t][i] = __builtin_nanf("");
+                    if (t0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > pos) sc[t][i] = kNone;
+                }
+        }
+        float mx = sc[0][0];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            if constexpr (I8) {
+        for (int i = 1; i < 32; ++i) mx = fmaxf(mx, sc[i >> 4][i & 15]);
+        if constexpr (!I8) mx *= scale2;
+        if (__any(mx > m + kLag)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            mx = fmaxf(mx, m);
+            const float f = mx == kNone ? 1.f : exp2_fast(m - mx);
+            m = mx;
+            l *= f;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+            for (int j = 0; j < kCols; ++j) acc[j] *= f;
+        }
+        const float base = m == kNone ? 0.f : m;
+        float w[32];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 f = *(const f32x4 *)(s_ks[buf] + 32 * t + 8 * g + 4 * half);
+        for (int i = 0; i < 32; ++i) {
+            const float x = sc[i >> 4][i & 15];
+            w[i] = exp2_fast(I8 ? x - base : __builtin_fmaf(x, scale2, -base));
+            l += w[i];
+        }
+        if constexpr (I8) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[rt][t][4 * g + e] *= f[e];
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 f = *(const f32x4 *)(s_vs[buf] + 32 * t + 8 * g + 4 * half);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = w[16 * t + 4 * g + e] * f[e];
+                        // an unseen token's scale may be anything
+                        w[16 * t + 4 * g + e] = CARE && sc[t][4 * g + e] == kNone ? 0.f : y;
                     }
-            }
-            if (bad) {
+                }
+        }
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (bad >> (2 * t + i / 8) & 1) sc[rt][t][i] = __builtin_nanf("");
-            }
-            if (masked) {
+            for (int j = 0; j < 4; ++j) pf[s][j] = pack_bf16(w[8 * s + 2 * j], w[8 * s + 2 * j + 1]);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + 32 * t + 8 * (i >> 2) + 4 * half + (i & 3) > pos[rt])
-                            sc[rt][t][i] = !I8 && p.scale2 < 0.f ? -kNone : kNone;
-            }
-            // the scores' maximum is the least of them under a negative scale
-            float mx = sc[rt][0][0];
-            if (!I8 && p.scale2 < 0.f) {
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mx = fminf(mx, sc[rt][i >> 4][i & 15]);
-            } else {
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mx = fmaxf(mx, sc[rt][i >> 4][i & 15]);
-            }
-            if constexpr (!I8) mx *= p.scale2;
-            if (__any(mx > m[rt] + kLag)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                mx = fmaxf(mx, m[rt]);
-                const float f = mx == kNone ? 1.f : exp2_fast(m[rt] - mx);
-                m[rt] = mx;
-                l[rt] *= f;
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) acc[rt][j] *= f;
-            }
-            const float base = m[rt] == kNone ? 0.f : m[rt];
-            float w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float x = sc[rt][i >> 4][i & 15];
-                w[i] = exp2_fast(I8 ? x - base : __builtin_fmaf(x, p.scale2, -base));
-                l[rt] += w[i];
-            }
-            if constexpr (I8) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 f = *(const f32x4 *)(s_vs[buf] + 32 * t + 8 * g + 4 * half);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y = w[16 * t + 4 * g + e] * f[e];
-                            // an unseen token's scale may be anything
-                            w[16 * t + 4 * g + e] = masked && sc[rt][t][4 * g + e] == kNone ? 0.f : y;
-                        }
-                    }
-            }
+        for (int j = 0; j < kCols; ++j) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
+                acc[j] = mfma32(vf[j & 1][s], pf[s], acc[j]);
+            if (j + 2 < kCols) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) pf[rt][s][j] = pack_bf16(w[8 * s + 2 * j], w[8 * s + 2 * j + 1]);
+                for (int s = 0; s < 4; ++s) vf[j & 1][s] = value(j + 2, s);
+                    }
         }
-        auto value = [&](int j, int s) {
-            const int d = 32 * j + c;
-            return *(const u32x4 *)(s_v[buf] + d * (kTile * 2) + (((2 * s + half) ^ ((d ^ d >> 3) & 7)) * 16));
-        };
-#pragma unroll
-        for (int j = 0; j < kCols; ++j)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const u32x4 a = value(j, s);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) acc[rt][j] = mfma32(a, pf[rt][s], acc[rt][j]);
-            }
     };
 
     if (tid < kWildWords) s_wild[tid] = 0u;
     __syncthreads();
     if (t_begin < t_end) {
         Staged g;
-        load(t_begin, number(t_begin), g);
-        int id = number(t_begin + kTile);
-        int bad = g.bad, buf = 0;
+        look_up(t_begin, number(t_begin));
+        load(t_begin, g);
+        int id = number(t_begin + kPlaces), bad = g.bad, buf = 0, t0 = t_begin;
         store(t_begin, g, 0);
-        for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
+        auto turn = [&](auto care) __attribute__((always_inline)) {
             __syncthreads();  // this tile is whole, the other buffer is free
-            const bool more = t0 + kTile < t_end;
+            const int next = t0 + kTile;
+            const bool more = next < t_end;
             if (more) {
-                load(t0 + kTile, id, g);
-                id = number(t0 + 2 * kTile);
+                if ((next - t_begin) % kPlaces == 0) {
+                    look_up(next, id);
+                    id = number(next + kPlaces);
+                }
+                load(next, g);
             }
-            if (t0 <= last_pos) compute(t0, buf, bad);  // else none of the wave's rows sees the tile
+            if (t0 <= last_pos) compute(t0, buf, bad, care);  // else none of the wave's rows sees the tile
             if (more) {
-                store(t0 + kTile, g, buf ^ 1);
+                store(next, g, buf ^ 1);
                 bad = g.bad;
             }
             buf ^= 1;
-        }
+            t0 = next;
+        };
+        // two loops, so that most tiles need neither masks nor the registers for them
+        while (t0 < t_end && t0 + kTile - 1 <= block_pos && !bad) turn(std::false_type{});
+        while (t0 < t_end) turn(std::true_type{});
     }
     if constexpr (!I8) {
         __syncthreads();
@@ -801,41 +806,34 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attn_tiles_kernel(const 
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float v = wild_part(((const uint16_t *)p.v)[at * D + 32 * j + 8 * (i >> 2) + 4 * half + (i & 3)]);
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            if (tok <= pos[rt]) acc[rt][j][i] += v;
+                        if (tok <= pos) acc[j][i] += v;
                     }
             }
     }
 
+    const float sum = l + __shfl_xor(l, 32, 64);
+    if (w0 + c > last) return;
+    const int64_t at = (int64_t)(sq.start + qi) * p.Hq + h * p.G + qg;
+    if (sh.used == 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = w0 + 32 * rt + c;
-        const float sum = l[rt] + __shfl_xor(l[rt], 32, 64);
-        if (r > last) continue;
-        const int i = r / p.G;
-        const int64_t at = (int64_t)(sq.start + i) * p.Hq + h * p.G + (r - i * p.G);
-        if (sh.used == 1) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int j = 0; j < kCols; ++j)
 #pragma unroll
-            for (int j = 0; j < kCols; ++j)
+            for (int g = 0; g < 4; ++g)
+                *(u32x2 *)(p.out + at * D + 32 * j + 8 * g + 4 * half) =
+                    u32x2{pack_bf16(acc[j][4 * g] * inv, acc[j][4 * g + 1] * inv),
+                          pack_bf16(acc[j][4 * g + 2] * inv, acc[j][4 * g + 3] * inv)};
+    } else {
+        const int64_t pr = (int64_t)split * p.T * p.Hq + at;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *(u32x2 *)(p.out + at * D + 32 * j + 8 * g + 4 * half) =
-                        u32x2{pack_bf16(acc[rt][j][4 * g] * inv, acc[rt][j][4 * g + 1] * inv),
-                              pack_bf16(acc[rt][j][4 * g + 2] * inv, acc[rt][j][4 * g + 3] * inv)};
-        } else {
-            const int64_t pr = (int64_t)split * p.T * p.Hq + at;
+        for (int j = 0; j < kCols; ++j)
 #pragma unroll
-            for (int j = 0; j < kCols; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *(f32x4 *)(p.part + pr * D + 32 * j + 8 * g + 4 * half) =
-                        f32x4{acc[rt][j][4 * g], acc[rt][j][4 * g + 1], acc[rt][j][4 * g + 2], acc[rt][j][4 * g + 3]};
-            if (half == 0) {
-                p.part_ml[pr * 2] = m[rt];
-                p.part_ml[pr * 2 + 1] = sum;
-            }
+            for (int g = 0; g < 4; ++g)
+                *(f32x4 *)(p.part + pr * D + 32 * j + 8 * g + 4 * half) =
+                    f32x4{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+        if (half == 0) {
+            p.part_ml[pr * 2] = m;
+            p.part_ml[pr * 2 + 1] = sum;
         }
     }
 }
@@ -900,7 +898,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int 
 // How a call is launched: rows of a workgroup, and which kernel takes them.
 struct Launch {
     bool tiles;
-    int rt;          // row tiles of a wave (16 rows, or 32 with tiles)
+    int rt;          // few rows: tiles of 16 rows of a workgroup
     int block_rows;  // rows of a workgroup
     int grain;       // tokens that splits are multiples of
 };
@@ -911,10 +909,7 @@ void launch_attention(const AttnParams &p, const Launch &k, int64_t B, int64_t m
 {
     const dim3 grid((unsigned)(row_blocks * p.splits), (unsigned)p.Hkv, (unsigned)B), block(256);
     if (k.tiles) {
-        if (k.rt == 1)
-            hipLaunchKernelGGL((attn_tiles_kernel<D, I8, 1>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((attn_tiles_kernel<D, I8, 2>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((attn_tiles_kernel<D, I8>), grid, block, 0, stream, p);
     } else {
         switch (k.rt) {
         case 1: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 1>), grid, block, 0, stream, p); break;
@@ -967,6 +962,10 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
                   "(0<=max_q<=T)", (long long)max_q, (long long)max_kv, (long long)table_width);
         return W4_ERR_SHAPE;
     }
+    if (!(fabsf(scale) <= 3.402823466e38f)) {
+        set_error("w4_paged_attention: scale is not finite");
+        return W4_ERR_SHAPE;
+    }
     if (T == 0 || B == 0 || max_q == 0) return W4_OK;
     if (!q || !k_cache || !v_cache || !q_start || !kv_len || !out || (table_width > 0 && !block_table) ||
         (cache_bits == 8 && (!k_scale || !v_scale))) {
@@ -996,13 +995,13 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
     Launch k;
     k.tiles = max_rows > 64;
     if (k.tiles)
-        k.rt = W4_TILES_RT, k.block_rows = 128 * k.rt, k.grain = kTile;
+        k.rt = 0, k.block_rows = kTileRows, k.grain = kTile;
     else
         k.rt = (int)((max_rows + 15) / 16), k.block_rows = 16 * k.rt, k.grain = kRowsGrain;
     const int64_t row_blocks = (max_rows + k.block_rows - 1) / k.block_rows;
     // one round of workgroups over the card, each with a grain of tokens or more
     const int64_t units = row_blocks * kv_heads * B, steps = (max_kv + k.grain - 1) / k.grain;
-    const int64_t room = (k.tiles ? k.rt == 1 : k.rt <= 2) ? 512 : 256;
+    const int64_t room = k.tiles || k.rt <= 2 ? 512 : 256;
     int64_t splits = room / units;
     if (splits > steps) splits = steps;
     if (splits > kMaxSplits) splits = kMaxSplits;

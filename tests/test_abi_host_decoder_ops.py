@@ -87,6 +87,7 @@ ATTN = dict(q=P[0], qt=3584, qh=128, kc=P[1], vc=P[2], ks=P[3], vs=P[4], bits=8,
     (dict(hkv=0), SHAPE), (dict(hq=27), SHAPE), (dict(hq=2), SHAPE), (dict(T=1 << 30), SHAPE), (dict(pages=0), SHAPE),
     (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE), (dict(page_size=8192), SHAPE), (dict(pages=1 << 38), SHAPE),
     (dict(width=-1), SHAPE), (dict(ts=15), SHAPE), (dict(max_q=11), SHAPE), (dict(max_q=-1), SHAPE),
+    (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE),
     (dict(max_kv=-1), SHAPE), (dict(qt=-1), SHAPE), (dict(qh=1 << 33), SHAPE),
     (dict(q=P[0] + 1), ALIGN), (dict(kc=P[1] + 8), ALIGN), (dict(vc=P[2] + 8), ALIGN), (dict(ks=P[3] + 4), ALIGN),
     (dict(vs=P[4] + 4), ALIGN), (dict(table=P[5] + 2), ALIGN), (dict(q_start=P[6] + 2), ALIGN),

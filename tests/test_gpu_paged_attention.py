@@ -176,6 +176,27 @@ def test_strides_scale_and_out(n):
     c.check(c.run(scale=-0.2), "negative scale", scale=-0.2)
 
 
+@pytest.mark.parametrize("n", [4, 100])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_scale_zero_and_values_of_all_kinds(n, bits):
+    # a scale of 0 weighs all seen tokens alike; infinite and NaN values reach the rows that see them
+    c = Case([n], [n + 70], 4, 2, 64, 16, bits, seed=21)
+    log(f"attention scale 0 n={n} bits={bits}")
+    c.check(c.run(scale=0.0), "scale 0", scale=0.0)
+    if bits == 8:
+        return
+    good, vc = c.run(), c.cache[1]
+    inf = float("inf")
+    for j, cols, value in ((2, 1, inf), (70 + n // 2, 5, -inf), (70 + n - 1, 9, float("nan"))):
+        vc[int(c.table[0, j // 16]), :, j % 16, cols] = value
+    got = c.run()
+    assert (got[:, :, 1] == inf).all()
+    assert (got[n // 2:, :, 5] == -inf).all() and torch.equal(got[:n // 2, :, 5], good[:n // 2, :, 5])
+    assert torch.isnan(got[n - 1, :, 9]).all() and torch.equal(got[:n - 1, :, 9], good[:n - 1, :, 9])
+    rest = [d for d in range(64) if d not in (1, 5, 9)]
+    assert torch.equal(got[:, :, rest], good[:, :, rest])
+
+
 @pytest.mark.parametrize("n", [2, 80])
 @pytest.mark.parametrize("bits", [16, 8])
 def test_bad_pages_give_nan_where_they_are_seen(n, bits):
