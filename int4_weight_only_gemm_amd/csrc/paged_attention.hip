@@ -24,7 +24,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kBlock = 32;        // tokens of one step of a wave (few rows)
-constexpr int kRowsGrain = 4 * kBlock;
 constexpr int kTile = 64;         // tokens of one step of a workgroup (many rows)
 constexpr int kTileRows = 128;    // rows of such a workgroup
 constexpr int kMaxSplits = 64;
@@ -62,18 +61,17 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int b)
     return s;
 }
 
-// How a row block's tokens are shared out over splits, in grains: `per` tokens for each used split
-// but the last.
+// How a row block's tokens are shared out over splits: evenly, in blocks of `unit` tokens, at least
+// `least` of them each.
 struct Share {
-    int per, used;
+    int blocks, used;
+    __device__ __forceinline__ int first(int split) const { return (int)((int64_t)blocks * split / used); }
 };
-__device__ __forceinline__ Share share_of(int tokens, int splits, int grain)
+__device__ __forceinline__ Share share_of(int tokens, int splits, int unit, int least)
 {
-    const int grains = (tokens + grain - 1) / grain;
     Share s;
-    s.per = max(1, (grains + splits - 1) / splits);
-    s.used = max(1, (grains + s.per - 1) / s.per);
-    s.per *= grain;
+    s.blocks = (int)(((int64_t)tokens + unit - 1) / unit);
+    s.used = min(splits, max(1, s.blocks / least));
     return s;
 }
 
@@ -163,15 +161,21 @@ struct ValueRegs {
     f32x4 s[2];
 };
 
+// Workgroups a CU holds.  With 8-bit pages, 48 rows fit the registers of two if the next keys are
+// not loaded ahead (five verified tokens over 16387, 28/4 heads: the same time, with twice the
+// waves to hide latency in larger batches).
+constexpr bool two_a_cu(int rt, bool i8) { return rt <= 2 || (rt == 3 && i8); }
+
 template <int D, bool I8, int RT>
-__global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const AttnParams p)
+__global__ __launch_bounds__(256, two_a_cu(RT, I8) ? 2 : 1) void attn_rows_kernel(const AttnParams p)
 {
     constexpr int kSteps = D / 32;        // k-steps of the scores
     constexpr int kCols = D / 16;         // columns of V a lane holds = output tiles
     constexpr int kRowPad = D + 4;
     __shared__ __align__(16) float s_o[4][16 * kRowPad];
     __shared__ float s_m[4][16 * RT], s_l[4][16 * RT];
-    __shared__ uint32_t s_wild[kWildWords];
+    constexpr int kWords = 4;             // noted tokens lie within 64 positions and a step
+    __shared__ uint32_t s_wild[4][kWords];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, quad = lane >> 4;
     const int split = blockIdx.x % p.splits, rb = blockIdx.x / p.splits, h = blockIdx.y, b = blockIdx.z;
@@ -180,10 +184,28 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
     if (r0 >= rows) return;
     const int last = min(rows, r0 + 16 * RT) - 1;
     const int tokens = tokens_of(sq, last, p.G);
-    const Share sh = share_of(tokens, p.splits, kRowsGrain);
+    const Share sh = share_of(tokens, p.splits, kBlock, 4);
     if (split >= sh.used) return;
-    const int blk_end = (min(tokens, (split + 1) * sh.per) + kBlock - 1) / kBlock;
+    const int blk_end = sh.first(split + 1);
     const int first_pos = sq.kv - sq.n + r0 / p.G;   // the least position of the rows
+    const int wild_from = max(first_pos, 0) / kBlock * kBlock;  // no step before it has a token that a row does not see
+    if (lane < kWords) s_wild[wave][lane] = 0u;
+
+    // The first steps' page numbers are asked for before the queries.
+    const int last_tile = (tokens - 1) / 16;
+    auto number = [&](int blk) { return page_number(p, b, min(2 * blk + (lane & 1), last_tile)); };
+    auto rows_of = [&](int blk, int id, int64_t (&row)[2]) {
+        const int64_t at = tile_row(p, h, min(2 * blk + (lane & 1), last_tile), id);
+        row[0] = lane_value(at, 0);
+        row[1] = lane_value(at, 1);
+    };
+    int blk = sh.first(split) + wave;
+    const bool any = blk < blk_end;
+    int id = -1, id_next = -1;
+    if (any) {
+        id = number(blk);
+        id_next = number(min(blk + 4, blk_end - 1));
+    }
 
     // queries: row c of each row tile, the columns of operand B's step
     u32x4 qf[RT][kSteps];
@@ -218,14 +240,6 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         l[rt] = 0.f;
     }
 
-    const int last_tile = (tokens - 1) / 16;
-    auto number = [&](int blk) { return page_number(p, b, min(2 * blk + (lane & 1), last_tile)); };
-    auto rows_of = [&](int blk, int id, int64_t (&row)[2]) {
-        const int64_t at = tile_row(p, h, min(2 * blk + (lane & 1), last_tile), id);
-        row[0] = lane_value(at, 0);
-        row[1] = lane_value(at, 1);
-    };
-    const int wild_from = max(first_pos, 0) / kBlock * kBlock;  // no step before it has a token that a row does not see
     auto load_k = [&](const int64_t (&row)[2], KeyRegs<D, I8> &kr) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -266,8 +280,16 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         }
     };
 
-    auto step = [&](int blk, const int64_t (&row)[2], const KeyRegs<D, I8> &kr, ValueRegs<D, I8> &vr) {
+    auto step = [&](int blk, const int64_t (&row)[2], KeyRegs<D, I8> &kr, ValueRegs<D, I8> &vr) {
         const int t0 = blk * kBlock;
+        // Codes are widened where they are used, not a step earlier (twice the registers) and not
+        // before the softmax (which would wait for the values there).
+        if constexpr (I8) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int s = 0; s < D / 64; ++s) asm volatile("" : "+v"(kr.k[t][s]));
+        }
         const bool masked = t0 + kBlock - 1 > first_pos;       // some row does not see some token
         const bool bad0 = row[0] < 0, bad1 = row[1] < 0;
         u32x4 pf[RT];
@@ -337,7 +359,12 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 #pragma unroll
             for (int e = 0; e < 4; ++e) pf[rt][e] = pack_bf16(w[2 * e], w[2 * e + 1]);
         }
-        if constexpr (!I8) {
+        if constexpr (I8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) asm volatile("" : "+v"(vr.v[e][j]));
+        } else {
             if (masked || bad0 || bad1) {
                 // What lies behind the sequence's end in its last page, and what a bad page number
                 // stands for, may be anything.
@@ -349,7 +376,7 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j)
                         vr.v[e][j] = none ? 0u : masked ? clear_wild(vr.v[e][j], odd) : vr.v[e][j];
-                    if (odd) atomicOr(&s_wild[(tok - wild_from) / 32 % kWildWords], 1u << (tok - wild_from) % 32);
+                    if (odd) atomicOr(&s_wild[wave][(tok - wild_from) / 32 % kWords], 1u << (tok - wild_from) % 32);
                 }
             }
         }
@@ -369,25 +396,31 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         }
     };
 
-    if (threadIdx.x < kWildWords) s_wild[threadIdx.x] = 0u;
-    __syncthreads();
-    int blk = split * (sh.per / kBlock) + wave;
-    if (blk < blk_end) {
+    if (any) {
+        // The next step's loads go out before a step is computed, where the registers for them are
+        // there.
+        constexpr bool kKeysAhead = !(RT == 3 && I8 && D == 128);
+        constexpr bool kValuesAhead = kKeysAhead && (RT != 2 || D == 64);
         KeyRegs<D, I8> kr;
         ValueRegs<D, I8> vr;
         int64_t row[2], next[2];
-        rows_of(blk, number(blk), row);
-        int id = number(min(blk + 4, blk_end - 1));
+        rows_of(blk, id, row);
         load_k(row, kr);
+        if constexpr (kValuesAhead) load_v(row, vr);
         for (; blk < blk_end; blk += 4) {
-            load_v(row, vr);
+            if constexpr (!kValuesAhead) load_v(row, vr);
             KeyRegs<D, I8> kn;
-            const int ahead = min(blk + 4, blk_end - 1);
-            rows_of(ahead, id, next);
-            id = number(min(blk + 8, blk_end - 1));
-            load_k(next, kn);
+            ValueRegs<D, I8> vn;
+            rows_of(min(blk + 4, blk_end - 1), id_next, next);
+            id_next = number(min(blk + 8, blk_end - 1));
+            if constexpr (kKeysAhead) load_k(next, kn);
+            if constexpr (kValuesAhead) load_v(next, vn);
             step(blk, row, kr, vr);
-            kr = kn;
+            if constexpr (kKeysAhead)
+                kr = kn;
+            else
+                load_k(next, kr);
+            if constexpr (kValuesAhead) vr = vn;
             row[0] = next[0], row[1] = next[1];
         }
     }
@@ -403,6 +436,12 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         }
     }
     __syncthreads();
+    uint32_t wild[kWords], any_wild = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        wild[i] = s_wild[0][i] | s_wild[1][i] | s_wild[2][i] | s_wild[3][i];
+        any_wild |= wild[i];
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         if (r0 + 16 * rt > last) break;
@@ -412,9 +451,11 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
         const float f = m[rt] == kNone ? (l[rt] == l[rt] ? 0.f : 1.f) : exp2_fast(m[rt] - mx);
         if (rt) __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s_o[wave][c * kRowPad + (4 * quad + i) * kCols + j] = acc[rt][j][i] * f;
+            for (int j = 0; j < kCols; j += 4)
+                *(f32x4 *)(s_o[wave] + c * kRowPad + (4 * quad + i) * kCols + j) =
+                    f32x4{acc[rt][j][i], acc[rt][j + 1][i], acc[rt][j + 2][i], acc[rt][j + 3][i]} * f;
         __syncthreads();
         // 16 threads a row, D / 16 columns each
         const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * kCols;
@@ -427,10 +468,10 @@ __global__ __launch_bounds__(256, RT <= 2 ? 2 : 1) void attn_rows_kernel(const A
 #pragma unroll
                 for (int w = 1; w < 4; ++w) o[j] += s_o[w][row * kRowPad + col + j];
             }
-            if constexpr (!I8) {
-                // the rows of a block lie within 64 positions, and this split's steps may end before
-                for (int word = 0; word < kWildWords; ++word)
-                    for (uint32_t bits = s_wild[word]; bits; bits &= bits - 1) {
+            if (!I8 && any_wild) {
+#pragma unroll
+                for (int word = 0; word < kWords; ++word)
+                    for (uint32_t bits = wild[word]; bits; bits &= bits - 1) {
                         const int tok = wild_from + 32 * word + __builtin_ctz(bits);
                         if (tok > sq.kv - sq.n + r / p.G) continue;
                         const int64_t at = tile_row(p, h, tok / 16, page_number(p, b, tok / 16));
@@ -506,9 +547,9 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
     if (r0 >= rows) return;
     const int last = min(rows, r0 + kRows) - 1;
     const int tokens = tokens_of(sq, last, p.G);
-    const Share sh = share_of(tokens, p.splits, kTile);
+    const Share sh = share_of(tokens, p.splits, kTile, 1);
     if (split >= sh.used) return;
-    const int t_begin = split * sh.per, t_end = min(tokens, t_begin + sh.per);
+    const int t_begin = sh.first(split) * kTile, t_end = min(tokens, sh.first(split + 1) * kTile);
     const int w0 = r0 + wave * 32;              // the wave's first row
     const int last_pos = sq.kv - sq.n + min(w0 + 31, rows - 1) / p.G;
     const int block_pos = sq.kv - sq.n + r0 / p.G;   // the least position of the workgroup's rows
@@ -797,7 +838,8 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
     }
     if constexpr (!I8) {
         __syncthreads();
-        for (int word = 0; word < kWildWords; ++word)
+        const bool some = __any(lane < kWildWords && s_wild[lane % kWildWords] != 0u);
+        for (int word = 0; some && word < kWildWords; ++word)
             for (uint32_t bits = s_wild[word]; bits; bits &= bits - 1) {
                 const int tok = wild_from + 32 * word + __builtin_ctz(bits);
                 const int64_t at = tile_row(p, h, tok / 16, page_number(p, b, tok / 16)) + tok % 16;
@@ -838,57 +880,49 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
     }
 }
 
-// Joins the splits of a row, in split order within each of 8 shares: a workgroup a row, D / 4
-// lanes a split, all loads of a row in flight together.
+// Joins the splits of a row, in split order within each share: a workgroup a row, D / 4 lanes a
+// split, all loads of a row in flight together.  Each wave holds every split's maximum and sum, one
+// a lane.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int block_rows, int grain)
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int block_rows, int unit, int least)
 {
     constexpr int kLanes = D / 4, kShares = 256 / kLanes, kHeld = kMaxSplits / kShares;
-    __shared__ float s_f[kMaxSplits];
-    __shared__ float s_l[kMaxSplits];
+    static_assert(kMaxSplits == 64, "one split a lane");
     __shared__ __align__(16) f32x4 s_o[kShares][kLanes];
-    const int tid = threadIdx.x, part = tid / kLanes, col = tid % kLanes;
+    const int tid = threadIdx.x, lane = tid & 63, part = tid / kLanes, col = tid % kLanes;
     const int b = blockIdx.y, i = blockIdx.x / p.Hq, hq = blockIdx.x - i * p.Hq;
     const Seq sq = seq_of(p, b);
     if (i >= sq.n) return;
     const int r = i * p.G + hq % p.G;
     const int last = min(sq.n * p.G, (r / block_rows + 1) * block_rows) - 1;
-    const Share sh = share_of(tokens_of(sq, last, p.G), p.splits, grain);
+    const Share sh = share_of(tokens_of(sq, last, p.G), p.splits, unit, least);
     if (sh.used == 1) return;
     const int64_t at = (int64_t)(sq.start + i) * p.Hq + hq, stride = (int64_t)p.T * p.Hq;
+    float m = kNone, l = 0.f;
+    if (lane < sh.used) {
+        m = p.part_ml[(lane * stride + at) * 2];
+        l = p.part_ml[(lane * stride + at) * 2 + 1];
+    }
     f32x4 x[kHeld];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
         const int s = k * kShares + part;
+        x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (s < sh.used) x[k] = *(const f32x4 *)(p.part + (s * stride + at) * D + col * 4);
     }
-    float m = kNone, l = 0.f;
-    if (tid < sh.used) {
-        m = p.part_ml[(tid * stride + at) * 2];
-        l = p.part_ml[(tid * stride + at) * 2 + 1];
-        s_f[tid] = m;
-    }
-    __syncthreads();
-    float M = kNone;
-    for (int s = 0; s < sh.used; ++s) M = fmaxf(M, s_f[s]);
-    __syncthreads();
-    if (tid < sh.used) {
-        const float f = m == kNone ? 1.f : exp2_fast(m - M);  // no maximum: zeros or NaN
-        s_f[tid] = f;
-        s_l[tid] = l * f;
-    }
-    __syncthreads();
+    float M = m;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+    const float f = m == kNone ? 1.f : exp2_fast(m - M);  // no maximum: zeros or NaN
+    float L = l * f;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off, 64);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const int s = k * kShares + part;
-        if (s < sh.used) o += x[k] * s_f[s];
-    }
+    for (int k = 0; k < kHeld; ++k) o += x[k] * __shfl(f, k * kShares + part, 64);
     s_o[part][col] = o;
     __syncthreads();
     if (tid >= kLanes) return;
-    float L = 0.f;
-    for (int s = 0; s < sh.used; ++s) L += s_l[s];
 #pragma unroll
     for (int k = 1; k < kShares; ++k) o += s_o[k][col];
     const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -900,7 +934,7 @@ struct Launch {
     bool tiles;
     int rt;          // few rows: tiles of 16 rows of a workgroup
     int block_rows;  // rows of a workgroup
-    int grain;       // tokens that splits are multiples of
+    int unit, least; // how its tokens are shared out over splits (share_of)
 };
 
 template <int D, bool I8>
@@ -920,7 +954,7 @@ void launch_attention(const AttnParams &p, const Launch &k, int64_t B, int64_t m
     }
     if (p.splits > 1)
         hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(max_q * p.Hq), (unsigned)B), block, 0, stream, p,
-                           k.block_rows, k.grain);
+                           k.block_rows, k.unit, k.least);
 }
 
 }  // namespace
@@ -995,13 +1029,13 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
     Launch k;
     k.tiles = max_rows > 64;
     if (k.tiles)
-        k.rt = 0, k.block_rows = kTileRows, k.grain = kTile;
+        k.rt = 0, k.block_rows = kTileRows, k.unit = kTile, k.least = 1;
     else
-        k.rt = (int)((max_rows + 15) / 16), k.block_rows = 16 * k.rt, k.grain = kRowsGrain;
+        k.rt = (int)((max_rows + 15) / 16), k.block_rows = 16 * k.rt, k.unit = kBlock, k.least = 4;
     const int64_t row_blocks = (max_rows + k.block_rows - 1) / k.block_rows;
-    // one round of workgroups over the card, each with a grain of tokens or more
-    const int64_t units = row_blocks * kv_heads * B, steps = (max_kv + k.grain - 1) / k.grain;
-    const int64_t room = k.tiles || k.rt <= 2 ? 512 : 256;
+    // one round of workgroups over the card, as far as the tokens go
+    const int64_t units = row_blocks * kv_heads * B, steps = max_kv / (k.unit * k.least);
+    const int64_t room = k.tiles || two_a_cu(k.rt, cache_bits == 8) ? 512 : 256;
     int64_t splits = room / units;
     if (splits > steps) splits = steps;
     if (splits > kMaxSplits) splits = kMaxSplits;
