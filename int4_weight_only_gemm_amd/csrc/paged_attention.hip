@@ -547,7 +547,7 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
     if (r0 >= rows) return;
     const int last = min(rows, r0 + kRows) - 1;
     const int tokens = tokens_of(sq, last, p.G);
-    const Share sh = share_of(tokens, p.splits, kTile, 1);
+    const Share sh = share_of(tokens, p.splits, kTile, 2);
     if (split >= sh.used) return;
     const int t_begin = sh.first(split) * kTile, t_end = min(tokens, sh.first(split + 1) * kTile);
     const int w0 = r0 + wave * 32;              // the wave's first row
@@ -880,35 +880,43 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
     }
 }
 
-// Joins the splits of a row, in split order within each share: a workgroup a row, D / 4 lanes a
-// split, all loads of a row in flight together.  Each wave holds every split's maximum and sum, one
-// a lane.
-template <int D>
+// Joins the splits of a row, in split order within each share: D / 4 lanes a split, all loads of a
+// row in flight together.  Each wave holds every split's maximum and sum, one a lane.  ROWS rows a
+// workgroup: 1 for up to 64 splits (a few rows of a long context, where only latency counts), 4, one
+// a wave, for up to 8 (the many rows of a chunk: 14000 rows of 4 splits took 50 us with one each).
+constexpr int kFewSplits = 8;
+template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int block_rows, int unit, int least)
 {
-    constexpr int kLanes = D / 4, kShares = 256 / kLanes, kHeld = kMaxSplits / kShares;
+    constexpr int kLanes = D / 4, kShares = 256 / ROWS / kLanes;
+    constexpr int kHeld = (ROWS == 1 ? kMaxSplits : kFewSplits) / kShares;
     static_assert(kMaxSplits == 64, "one split a lane");
-    __shared__ __align__(16) f32x4 s_o[kShares][kLanes];
-    const int tid = threadIdx.x, lane = tid & 63, part = tid / kLanes, col = tid % kLanes;
-    const int b = blockIdx.y, i = blockIdx.x / p.Hq, hq = blockIdx.x - i * p.Hq;
+    __shared__ __align__(16) f32x4 s_o[256 / kLanes][kLanes];
+    const int tid = threadIdx.x, lane = tid & 63, share = tid / kLanes, part = share % kShares, col = tid % kLanes;
+    const int b = blockIdx.y, x = blockIdx.x * ROWS + (ROWS == 1 ? 0 : tid >> 6);
+    const int i = x / p.Hq, hq = x - i * p.Hq;
     const Seq sq = seq_of(p, b);
-    if (i >= sq.n) return;
-    const int r = i * p.G + hq % p.G;
-    const int last = min(sq.n * p.G, (r / block_rows + 1) * block_rows) - 1;
-    const Share sh = share_of(tokens_of(sq, last, p.G), p.splits, unit, least);
-    if (sh.used == 1) return;
-    const int64_t at = (int64_t)(sq.start + i) * p.Hq + hq, stride = (int64_t)p.T * p.Hq;
+    int used = 1;
+    int64_t at = 0;
+    const int64_t stride = (int64_t)p.T * p.Hq;
+    if (i < sq.n) {
+        const int r = i * p.G + hq % p.G;
+        const int last = min(sq.n * p.G, (r / block_rows + 1) * block_rows) - 1;
+        used = share_of(tokens_of(sq, last, p.G), p.splits, unit, least).used;
+        at = (int64_t)(sq.start + i) * p.Hq + hq;
+    }
+    // one split: the row is written already
     float m = kNone, l = 0.f;
-    if (lane < sh.used) {
+    if (used > 1 && lane < used) {
         m = p.part_ml[(lane * stride + at) * 2];
         l = p.part_ml[(lane * stride + at) * 2 + 1];
     }
-    f32x4 x[kHeld];
+    f32x4 v[kHeld];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
         const int s = k * kShares + part;
-        x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (s < sh.used) x[k] = *(const f32x4 *)(p.part + (s * stride + at) * D + col * 4);
+        v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (used > 1 && s < used) v[k] = *(const f32x4 *)(p.part + (s * stride + at) * D + col * 4);
     }
     float M = m;
 #pragma unroll
@@ -919,15 +927,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p, int 
     for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off, 64);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) o += x[k] * __shfl(f, k * kShares + part, 64);
-    s_o[part][col] = o;
+    for (int k = 0; k < kHeld; ++k) o += v[k] * __shfl(f, k * kShares + part, 64);
+    s_o[share][col] = o;
     __syncthreads();
-    if (tid >= kLanes) return;
+    if (part != 0 || used == 1) return;
 #pragma unroll
-    for (int k = 1; k < kShares; ++k) o += s_o[k][col];
+    for (int k = 1; k < kShares; ++k) o += s_o[share + k][col];
     const float inv = L == 0.f ? 0.f : 1.f / L;
     *(u32x2 *)(p.out + at * D + col * 4) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
+
+// Row tiles of 16 up to which the few-rows kernel is taken.  32 sequences of 1500 tokens, 16 heads
+// of 128, few-rows against tiles kernel: bfloat16 pages 61 and 70 us at 32 rows, 72 and 71 at 40, 78
+// and 72 at 64; 8-bit pages 42 and 69 us at 48 rows, 64 and 70 at 64.  Heads of 64 in bfloat16: 38
+// and 41 us at 40 rows, 52 and 41 at 64.
+constexpr int most_row_tiles(int D, bool i8) { return i8 ? 4 : D == 64 ? 3 : 2; }
 
 // How a call is launched: rows of a workgroup, and which kernel takes them.
 struct Launch {
@@ -944,17 +958,24 @@ void launch_attention(const AttnParams &p, const Launch &k, int64_t B, int64_t m
     const dim3 grid((unsigned)(row_blocks * p.splits), (unsigned)p.Hkv, (unsigned)B), block(256);
     if (k.tiles) {
         hipLaunchKernelGGL((attn_tiles_kernel<D, I8>), grid, block, 0, stream, p);
-    } else {
-        switch (k.rt) {
-        case 1: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 1>), grid, block, 0, stream, p); break;
-        case 2: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 2>), grid, block, 0, stream, p); break;
-        case 3: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 3>), grid, block, 0, stream, p); break;
-        default: hipLaunchKernelGGL((attn_rows_kernel<D, I8, 4>), grid, block, 0, stream, p); break;
+    } else if (k.rt == 1) {
+        hipLaunchKernelGGL((attn_rows_kernel<D, I8, 1>), grid, block, 0, stream, p);
+    } else if (k.rt == 2) {
+        hipLaunchKernelGGL((attn_rows_kernel<D, I8, 2>), grid, block, 0, stream, p);
+    } else if constexpr (most_row_tiles(D, I8) >= 3) {
+        if (k.rt == 3) {
+            hipLaunchKernelGGL((attn_rows_kernel<D, I8, 3>), grid, block, 0, stream, p);
+        } else if constexpr (most_row_tiles(D, I8) >= 4) {
+            hipLaunchKernelGGL((attn_rows_kernel<D, I8, 4>), grid, block, 0, stream, p);
         }
     }
-    if (p.splits > 1)
-        hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(max_q * p.Hq), (unsigned)B), block, 0, stream, p,
+    const int64_t rows = max_q * p.Hq;
+    if (p.splits > kFewSplits)
+        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)rows, (unsigned)B), block, 0, stream, p,
                            k.block_rows, k.unit, k.least);
+    else if (p.splits > 1)
+        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)((rows + 3) / 4), (unsigned)B), block, 0, stream,
+                           p, k.block_rows, k.unit, k.least);
 }
 
 }  // namespace
@@ -1027,16 +1048,19 @@ w4_status w4_paged_attention(const void *q, int64_t q_token_stride, int64_t q_he
     p.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     const int64_t max_rows = max_q * p.G;
     Launch k;
-    k.tiles = max_rows > 64;
+    k.tiles = max_rows > 16 * most_row_tiles((int)D, cache_bits == 8);
     if (k.tiles)
-        k.rt = 0, k.block_rows = kTileRows, k.unit = kTile, k.least = 1;
+        k.rt = 0, k.block_rows = kTileRows, k.unit = kTile, k.least = 2;
     else
         k.rt = (int)((max_rows + 15) / 16), k.block_rows = 16 * k.rt, k.unit = kBlock, k.least = 4;
     const int64_t row_blocks = (max_rows + k.block_rows - 1) / k.block_rows;
-    // one round of workgroups over the card, as far as the tokens go
-    const int64_t units = row_blocks * kv_heads * B, steps = max_kv / (k.unit * k.least);
-    const int64_t room = k.tiles || two_a_cu(k.rt, cache_bits == 8) ? 512 : 256;
-    int64_t splits = room / units;
+    // One round of workgroups over the card, as far as the tokens go.  Joining costs a workgroup a row
+    // beyond 8 splits: only for few rows (1000 rows of 16 splits 31 us, of 8 splits 35 us; 2000 rows
+    // 42 and 38 us), and then one tile workgroup a CU (500 rows: 26 us, with two 31 us).
+    const int64_t units = row_blocks * kv_heads * B, steps = max_kv / (k.unit * k.least), out_rows = T * q_heads;
+    int64_t splits = (k.tiles || two_a_cu(k.rt, cache_bits == 8) ? 512 : 256) / units;
+    if (k.tiles && splits > kFewSplits) splits = 256 / units > kFewSplits ? 256 / units : kFewSplits;
+    if (splits > kFewSplits && out_rows > 1280) splits = kFewSplits;
     if (splits > steps) splits = steps;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits < 1) splits = 1;
