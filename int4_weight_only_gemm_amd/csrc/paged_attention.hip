@@ -335,9 +335,9 @@ __global__ __launch_bounds__(256, two_a_cu(RT, I8) ? 2 : 1) void attn_rows_kerne
             if (__any(mx > m[rt] + kLag)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                mx = fmaxf(mx, m[rt]);
-                const float f = mx == kNone ? 1.f : exp2_fast(m[rt] - mx);
-                m[rt] = mx;
+                const bool up = mx > m[rt] + kLag;  // each row by its own scores alone
+                const float f = up ? exp2_fast(m[rt] - mx) : 1.f;
+                m[rt] = up ? mx : m[rt];
                 l[rt] *= f;
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) acc[rt][j] *= f;
@@ -760,9 +760,9 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(const AttnParams p)
         if constexpr (!I8) mx *= scale2;
         if (__any(mx > m + kLag)) {
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            mx = fmaxf(mx, m);
-            const float f = mx == kNone ? 1.f : exp2_fast(m - mx);
-            m = mx;
+            const bool up = mx > m + kLag;  // each row by its own scores alone
+            const float f = up ? exp2_fast(m - mx) : 1.f;
+            m = up ? mx : m;
             l *= f;
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] *= f;
