@@ -106,10 +106,18 @@ __device__ __forceinline__ float row16_fmax(float v)
 }
 
 // Symmetric code of x on a grid of step s: rint(x / s) within [lo, hi], IEEE division and
-// ties to even, 0 for an empty grid.
-__device__ __forceinline__ int symmetric_code(float x, float s, float lo, float hi)
+// ties to even, 0 for an empty grid.  r = 1 / s, correctly rounded.  With |x / s| below 128, x * r
+// is within 2^-16 of the exact quotient and the rounded quotient within 2^-18, so both round to the
+// same integer unless the quotient lies within 2^-15 of a half-integer: those few take the division
+// (a branch that waves skip when none of their lanes needs it), as do quotients that are no
+// numbers (a step so small that r is infinite).  A division each made the write of 8191 tokens of 32
+// heads of 128 take 57 us, against 51 us.
+__device__ __forceinline__ int symmetric_code(float x, float s, float r, float lo, float hi)
 {
-    return s == 0.0f ? 0 : (int)fminf(fmaxf(rintf(x / s), lo), hi);
+    const float u = x * r;
+    float q = rintf(u);
+    if (__builtin_expect(!(fabsf(u - (floorf(u) + 0.5f)) >= 0x1p-15f), 0)) q = rintf(x / s);
+    return s == 0.0f ? 0 : (int)fminf(fmaxf(q, lo), hi);
 }
 
 }  // namespace w4dev

@@ -179,18 +179,18 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(const NormParams 
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
         top = row16_fmax(top);
-        const float s = top / (p.bits == 4 ? 7.0f : 127.0f);
+        const float s = top / (p.bits == 4 ? 7.0f : 127.0f), back = 1.0f / s;
         if (e < p.H) {
             if (p.bits == 4) {
                 uint32_t word = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) word |= (uint32_t)(symmetric_code(y[j], s, -8.f, 7.f) + 8) << (4 * j);
+                for (int j = 0; j < 8; ++j) word |= (uint32_t)(symmetric_code(y[j], s, back, -8.f, 7.f) + 8) << (4 * j);
                 ((uint32_t *)p.y)[(ob + e) >> 3] = word;
             } else {
                 u32x2 word = {0u, 0u};
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    word[j >> 2] |= (uint32_t)(symmetric_code(y[j], s, -127.f, 127.f) & 0xFF) << (8 * (j & 3));
+                    word[j >> 2] |= (uint32_t)(symmetric_code(y[j], s, back, -127.f, 127.f) & 0xFF) << (8 * (j & 3));
                 *(u32x2 *)((uint8_t *)p.y + ob + e) = word;
             }
             if ((tid & 15) == 0) p.scales[(ob + e) / kGroup] = s;

@@ -28,7 +28,8 @@ def pools(pages, heads, page, D, bits, g):
 
 
 CASES = [(1, 1, 64, 1, 3), (5, 4, 128, 64, 4), (17, 2, 128, 16, 9), (100, 3, 64, 48, 5), (257, 32, 128, 16, 20),
-         (40, 8, 64, 7, 11), (1000, 1, 128, 256, 6)]
+         (40, 8, 64, 7, 11), (1000, 1, 128, 256, 6),
+         (17001, 9, 128, 64, 270), (40003, 7, 64, 96, 420)]  # the last two: four heads a thread
 
 
 @pytest.mark.parametrize("T,heads,D,page,pages", CASES)
@@ -111,6 +112,29 @@ def test_slots_past_32_bits():
     q, s = expected(v, 8)
     assert torch.equal(v2.cpu(), q.float() * s[..., None])
     assert int(kc.ne(0).any(-1).any(1).sum()) == 3        # three tokens, and no other place
+
+
+def test_codes_at_borders():
+    # quotients at and next to half-integers, steps from the smallest to the largest, bit for bit
+    g = torch.Generator().manual_seed(23)
+    rows = []
+    for e in (-149, -140, -126, -100, -20, 0, 20, 100, 121):
+        top = 127.0 * 2.0 ** e if e > -140 else 2.0 ** e * 50
+        k = torch.randint(-127, 127, (40, 128), generator=g) + 0.5
+        x = (k * 2.0 ** e).float()
+        x = torch.where(torch.rand(40, 128, generator=g) < 0.5, x, torch.nextafter(x, torch.zeros(())))
+        x[:, 0] = top
+        rows.append(x)
+    x = torch.cat(rows + [torch.randn(64, 128, generator=g) * 10.0 ** torch.randint(-44, 38, (64, 1), generator=g)])
+    T = x.shape[0]
+    k = x.view(T, 1, 128)
+    c = [torch.zeros(T // 16 + 1, 1, 16, 128, dtype=torch.int8, device="cuda") for _ in range(2)]
+    s = [torch.zeros(T // 16 + 1, 1, 16, device="cuda") for _ in range(2)]
+    log("kv codes at borders")
+    w4.kv_write(k.cuda(), k.cuda(), torch.arange(T).cuda(), *c, *s)
+    q, want = expected(k, 8)
+    assert torch.equal(s[0].cpu().view(-1)[:T], want.view(-1))
+    assert torch.equal(c[0].cpu().view(-1, 128)[:T], q.view(T, 128))
 
 
 def test_empty_streams_and_refusals():
