@@ -24,14 +24,17 @@
 //      bins in which the cuts fall, and the exact ranks of the few tokens inside those bins the
 //      cut.  Then sums of kept weight by tiles give the tile of the token, which is read again.
 //   2., 3. Rows whose cuts lie deeper (flat distributions, large k, thousands of equal logits):
-//      the same from the whole row, one pass for the bins and one for what lies above and
-//      inside the cuts' bins.  Other rows' workgroups leave at once.
+//      the same from the whole row with bins of 1/128 nat, one pass for the bins and one for what
+//      lies above and inside the cuts' bins (in steps of 256 shares of their range where that is more
+//      than a list holds: long runs of equal logits).  Other rows' workgroups leave at once.
 // Each row is split into chunks over workgroups; the last workgroup of a row to arrive does
 // the row's serial part.  Workgroups are small (4 waves) for its sake: with 16 waves each of its
 // steps took four times as long (one row of 152064: 26 us in all, 19 us with 4 waves).
 //
-// Measured: 160 rows of 152064 float32 logits with mixed settings 71 us for all three launches
-// (97 MB: one read at the rate of a large copy is 19 us), one row 24 us.
+// Measured, all launches: 160 rows of 152064 float32 logits with mixed settings 55 to 60 us where
+// every row's cuts lie in its list (97 MB: one read at the rate of a large copy is 19 us; the
+// list, the sums and the serial parts take the rest), 115 to 165 us where one or more rows take
+// the general passes (30 us each, mostly the latency of their serial parts); one row 24 us.
 #include "internal.h"
 
 using namespace w4host;
@@ -41,9 +44,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 1024;            // the last one also takes all that lies further below
-constexpr float kBinsPerNat = 32.0f;   // 32 nats: a weight below 2^-46 of the largest rounds to 0
-constexpr int kNear = 288;             // bins of the weights above e^-9
+constexpr int kNats = 32;              // a weight below e^-32 = 2^-46 of the largest rounds to 0
+constexpr int kNearNats = 9;           // weights above e^-9 take the full series
+constexpr int kBins = 4096;            // of the whole row; the last one also takes all that lies further below
+constexpr int kListBins = 1024;        // of pass 1's list
+constexpr int kNear = kBins / kNats * kNearNats;
 constexpr int kTile = kThreads * 4;    // tokens a workgroup reads at a time
 constexpr int kAhead = 4;              // tiles in flight
 constexpr int kMinChunk = kAhead * kTile;
@@ -147,6 +152,7 @@ struct Row {
     float top, bin_scale;
     double per_log2;  // log2(e) / T
     float min_p;
+    int last;       // the last bin
     int near_bins;  // bins whose weights take the full series
 };
 
@@ -154,7 +160,7 @@ struct Row {
 // infinite one times a scale of 0, takes the last bin.
 __device__ __forceinline__ int bin_of(float l, const Row &r)
 {
-    return (int)fminf((r.top - l) * r.bin_scale, (float)(kBins - 1));
+    return (int)fminf((r.top - l) * r.bin_scale, (float)r.last);
 }
 
 // 2^x * 2^44 for |x| <= 1000; the weight of a logit outside the last bin, exp((l - top) / T), in
@@ -326,14 +332,15 @@ __device__ __forceinline__ Settings settings_of(const SampleParams &p, int b)
     return s;
 }
 
-__device__ __forceinline__ Row row_of(const Settings &s, float top)
+__device__ __forceinline__ Row row_of(const Settings &s, float top, int bins)
 {
     Row r;
     r.top = top;
     r.per_log2 = 1.4426950408889634 / (double)s.t;
-    r.bin_scale = fminf(kBinsPerNat / s.t, kMost);
+    r.bin_scale = fminf((float)(bins / kNats) / s.t, kMost);
+    r.last = bins - 1;
     r.min_p = s.min_p > 0.f ? fminf(s.min_p, 1.f) : 0.f;
-    r.near_bins = r.min_p > 0.f ? kBins : kNear;
+    r.near_bins = r.min_p > 0.f ? bins : bins / kNats * kNearNats;
     return r;
 }
 
@@ -342,14 +349,14 @@ __device__ __forceinline__ const void *row_ptr(const SampleParams &p, int b, boo
     return (const char *)p.logits + (int64_t)b * p.stride * (f32 ? 4 : 2);
 }
 
-constexpr int kPer = kBins / kThreads;
 
-// The bins in which the cuts fall, from each thread's kPer bins (n: counts, w: weight sums).
+// The bins in which the cuts fall (kBins: none), from each thread's kPer bins (n: counts, w: weight sums).
 // `all`: the row's weight where top-k does not bound it.  *cut is in LDS; ends with a barrier.
 struct FindBins {
     unsigned long long w[kWaves], w1[2];
     unsigned n[kWaves];
 };
+template <int kPer>
 __device__ __forceinline__ void find_bins(const unsigned (&n)[kPer], const unsigned long long (&w)[kPer], int k,
                                           float top_p, int V, bool sum_is_all, double all, RowCut *cut, FindBins *s)
 {
@@ -544,7 +551,7 @@ __device__ __forceinline__ void draw_token(const SampleParams &p, int b, const v
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int bin = bin_of(l[j], r);
-        w[j] = bin == kBins - 1 || (bin >= sure_end && place_of(l[j], e + j) > last_place) ? 0ull
+        w[j] = bin == r.last || (bin >= sure_end && place_of(l[j], e + j) > last_place) ? 0ull
                                                                                            : drawn_weight(l[j], bin, r);
         mine += w[j];
     }
@@ -571,8 +578,8 @@ template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParams p)
 {
     struct Hist {
-        unsigned long long w[kBins];
-        unsigned n[kBins];
+        unsigned long long w[kListBins];
+        unsigned n[kListBins];
     };
     union Work {
         Hist hist;                   // dead once its bins are in registers
@@ -716,7 +723,7 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
         }
         return;
     }
-    const Row r = row_of(set, top);
+    const Row r = row_of(set, top, kListBins);
     double all = 0.0;  // the row's weight in units
     bool settled = true;
     if (sum_all) {
@@ -749,7 +756,7 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int bin = bin_of(l[j], r);
-                w[j] = bin == kBins - 1 ? 0ull : fixed_weight(l[j], bin, r);
+                w[j] = bin == r.last ? 0ull : fixed_weight(l[j], bin, r);
                 mine += w[j];
             }
             unsigned long long run = wave_scan(mine);
@@ -786,7 +793,7 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
 
     // The tokens above every chunk's threshold, one behind the other: the list is complete down to
     // there.
-    for (int i = tid; i < kBins; i += kThreads) {
+    for (int i = tid; i < kListBins; i += kThreads) {
         s_work.hist.w[i] = 0ull;
         s_work.hist.n[i] = 0u;
     }
@@ -803,7 +810,7 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
     const bool whole_row = least == kNone;
     settled = settled && n > 0 && n <= kOwn && (whole_row || !cut_k || n >= (unsigned)set.k);
     if (settled && !cut_k && !cut_p)  // min-p alone: does the list reach below it
-        settled = whole_row || bin_of(least, r) == kBins - 1 ||
+        settled = whole_row || bin_of(least, r) == r.last ||
                   weight_of(least, r) < (double)r.min_p * kUnit * (1.0 - 1e-9);
     if (settled) {
         unsigned long long last_place = ~0ull;
@@ -812,12 +819,13 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
             for (unsigned i = tid; i < n; i += kThreads) {
                 const float l = logit_of(s_place[i]);
                 const int bin = bin_of(l, r);
-                if (bin == kBins - 1) continue;
+                if (bin == r.last) continue;
                 atomicAdd(&s_work.hist.n[bin], 1u);
                 atomicAdd(&s_work.hist.w[bin], fixed_weight(l, bin, r));
             }
             if (tid == 0) s_inside = 0u;
             __syncthreads();
+            constexpr int kPer = kListBins / kThreads;
             unsigned nb[kPer];
             unsigned long long wb[kPer];
 #pragma unroll
@@ -842,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void sample_list_kernel(const SampleParam
             for (unsigned i = tid; i < n; i += kThreads) {
                 const float l = logit_of(s_place[i]);
                 const int bin = bin_of(l, r);
-                if (bin != kBins - 1 && (bin < sure_end || s_place[i] <= last_place))
+                if (bin != r.last && (bin < sure_end || s_place[i] <= last_place))
                     atomicAdd(&s_sum[(uint32_t)s_place[i] / kTile], drawn_weight(l, bin, r));
             }
             draw_token<F32, VEC>(p, b, row, r, set.u, sure_end, last_place, s_sum, tiles, s);
@@ -874,28 +882,32 @@ __global__ __launch_bounds__(kThreads) void sample_bins_kernel(const SampleParam
     const Settings set = settings_of(p, b);
     const int begin = c * p.chunk_len, end = min(p.V, begin + p.chunk_len);
     const void *row = row_ptr(p, b, F32);
-    f32x4 ahead = logits4<F32, VEC>(row, begin + tid * 4, end);
+    f32x4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = logits4<F32, VEC>(row, begin + i * kTile + tid * 4, end);
     const float top = logit_of(row_top(p, b));
     const int k = set.k;
     const float top_p = set.top_p;
     const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
     if (!cut_k && !cut_p) return;  // nothing to find
-    const Row r = row_of(set, top);
+    const Row r = row_of(set, top, kBins);
     for (int i = tid; i < kBins; i += kThreads) {
         s_w[i] = 0ull;
         if (i < kNear) s_n[i] = 0u;
     }
     __syncthreads();
     for (int e = begin + tid * 4; e < end; e += kTile) {
-        const f32x4 l = ahead;
-        ahead = logits4<F32, VEC>(row, e + kTile, end);  // -infinity past the end: the last bin
+        const f32x4 l = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = logits4<F32, VEC>(row, e + kAhead * kTile, end);  // -infinity past the end: the last bin
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int bin = bin_of(l[j], r);
             if (bin < kNear) {
                 atomicAdd(&s_n[bin], 1u);
                 if (cut_p) atomicAdd(&s_w[bin], fixed_weight(l[j], bin, r));
-            } else if (bin < kBins - 1) {  // the last weighs nothing and needs no count
+            } else if (bin < r.last) {  // the last weighs nothing and needs no count
                 atomicAdd(&s_w[bin], (1ull << 48) | (cut_p ? fixed_weight<true>(l[j], bin, r) : 0ull));
             }
         }
@@ -912,6 +924,7 @@ __global__ __launch_bounds__(kThreads) void sample_bins_kernel(const SampleParam
     }
     if (!last_to_arrive(p.arrive + gridDim.y + b, p.chunks, &s_last)) return;
 
+    constexpr int kPer = kBins / kThreads;
     unsigned n[kPer];
     unsigned long long w[kPer];
 #pragma unroll
@@ -931,6 +944,11 @@ template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParams p)
 {
     __shared__ Inside<kInside> s_inside;
+    __shared__ struct {
+        unsigned long long w[kThreads], n_wave[kWaves], w_wave[kWaves];
+        unsigned n[kThreads];
+        int pick;
+    } s_step;
     __shared__ unsigned long long s_sum[kMaxTiles];
     __shared__ unsigned long long s[kWaves];
     __shared__ unsigned s_count, s_base, s_last;
@@ -940,13 +958,15 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
     const Settings set = settings_of(p, b);
     const int begin = c * p.chunk_len, end = min(p.V, begin + p.chunk_len);
     const void *row = row_ptr(p, b, F32);
-    f32x4 ahead = logits4<F32, VEC>(row, begin + tid * 4, end);
+    f32x4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = logits4<F32, VEC>(row, begin + i * kTile + tid * 4, end);
     const unsigned long long best = row_top(p, b);
     const float top = logit_of(best);
     const int k = set.k;
     const float top_p = set.top_p;
     const bool cut_k = k > 0 && k < p.V, cut_p = top_p < 1.f;
-    const Row r = row_of(set, top);
+    const Row r = row_of(set, top, kBins);
     if (!cut_k && !cut_p) cut.sure_end = kBins, cut.lo = kBins, cut.hi = -1, cut.bin_k = -1;
     const int tiles = (p.V + kTile - 1) / kTile;
     if (tid == 0) s_count = 0u;
@@ -954,13 +974,15 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
     __syncthreads();
     for (int e0 = begin; e0 < end; e0 += kTile) {
         const int e = e0 + tid * 4;
-        const f32x4 l = ahead;
-        ahead = logits4<F32, VEC>(row, e + kTile, end);
+        const f32x4 l = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = logits4<F32, VEC>(row, e + kAhead * kTile, end);
         unsigned long long mine = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int bin = bin_of(l[j], r);
-            if (bin == kBins - 1) continue;
+            if (bin == r.last) continue;
             if (bin < cut.sure_end) {
                 mine += drawn_weight<true>(l[j], bin, r);
             } else if (inside(bin, cut)) {
@@ -1001,57 +1023,78 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
                 if (n * kThreads + tid < listed) put_inside(s_inside, n * kThreads + tid, place[n], cut, r);
             last_place = cut_of(s_inside, listed, cut, top_p, best, s);
         } else {
-            // More tokens in the cuts' bins than the list holds (thousands of equal or nearly
-            // equal logits): halve the range of places until the cut is found, each step one
-            // pass over the row.
-            auto count_and_sum = [&](unsigned long long upto, int from, int to, unsigned long long *n_out,
-                                     unsigned long long *w_out) {
-                unsigned long long n = 0, w = 0;
-                for (int e = tid * 4; e < p.V; e += kTile) {
-                    const f32x4 l = logits4<F32, VEC>(row, e, p.V);
+            // More tokens in the cuts' bins than the list holds (thousands of equal or nearly equal
+            // logits): the cut's place by halving its range, 8 times a pass over the row.  Returns the
+            // smallest place up to which the tokens of the bins from..to count `count` or, if that is 0,
+            // weigh with `before` at least `want`; *weight: what they weigh up to it.
+            auto search = [&](int from, int to, unsigned count, double want, unsigned long long before,
+                              unsigned long long lo, unsigned long long hi, unsigned long long *weight) {
+                unsigned long long n_below = 0, w_below = 0;
+                for (;;) {
+                    const int shift = max(0, 56 - __builtin_clzll((hi - lo) | 1ull));  // 256 shares or fewer
+                    s_step.w[tid] = 0ull;
+                    s_step.n[tid] = 0u;
+                    if (tid == 0) s_step.pick = (int)((hi - lo) >> shift);  // the last share, should rounding reach none
+                    __syncthreads();
+                    for (int e = tid * 4; e < p.V; e += kTile) {
+                        const f32x4 l = logits4<F32, VEC>(row, e, p.V);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (e + j >= p.V || place_of(l[j], e + j) > upto) continue;
-                        const int bin = bin_of(l[j], r);
-                        if (bin < from || bin > to || bin == kBins - 1) continue;
-                        ++n;
-                        w += fixed_weight(l[j], bin, r);
+                        for (int j = 0; j < 4; ++j) {
+                            const unsigned long long at = place_of(l[j], e + j);
+                            const int bin = bin_of(l[j], r);
+                            if (e + j >= p.V || at < lo || at > hi || bin < from || bin > to || bin == r.last) continue;
+                            atomicAdd(&s_step.n[(at - lo) >> shift], 1u);
+                            atomicAdd(&s_step.w[(at - lo) >> shift], fixed_weight(l[j], bin, r));
+                        }
+                    }
+                    __syncthreads();
+                    // one share a thread: the first up to which the target is reached
+                    const unsigned long long n_own = s_step.n[tid], w_own = s_step.w[tid];
+                    unsigned long long n = wave_scan(n_own), w = wave_scan(w_own);
+                    if (lane == 63) s_step.n_wave[tid >> 6] = n, s_step.w_wave[tid >> 6] = w;
+                    __syncthreads();
+                    for (int i = 0; i < tid >> 6; ++i) n += s_step.n_wave[i], w += s_step.w_wave[i];
+                    const bool there = count ? n_below + n >= count : (double)(before + w_below + w) >= want;
+                    if (there) atomicMin(&s_step.pick, tid);
+                    __syncthreads();
+                    const int pick = s_step.pick;
+                    if (tid == pick) {
+                        s_step.n_wave[0] = n - n_own, s_step.w_wave[0] = w - w_own;
+                        s_step.w_wave[1] = w;
+                    }
+                    __syncthreads();
+                    const unsigned long long through = w_below + s_step.w_wave[1];
+                    n_below += s_step.n_wave[0];
+                    w_below += s_step.w_wave[0];
+                    lo += (unsigned long long)pick << shift;
+                    hi = min(hi, lo + ((1ull << shift) - 1));
+                    __syncthreads();
+                    if (shift == 0) {
+                        *weight = through;
+                        return lo;
                     }
                 }
-                *n_out = block_sum(n, s);
-                *w_out = block_sum(w, s);
             };
-            unsigned long long n, w, lo, hi, kept = ~0ull;
+            // the range of places of the bins' tokens
+            unsigned long long lo = ~0ull, hi = 0ull, kept = ~0ull, w = 0ull;
+            for (int e = tid * 4; e < p.V; e += kTile) {
+                const f32x4 l = logits4<F32, VEC>(row, e, p.V);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned long long at = place_of(l[j], e + j);
+                    if (e + j >= p.V || !inside(bin_of(l[j], r), cut)) continue;
+                    lo = min(lo, at);
+                    hi = max(hi, at);
+                }
+            }
+            lo = block_min(lo, s);
+            hi = ~block_min(~hi, s);
             double all = cut.sum_all;
             if (cut.bin_k >= 0) {
-                // the smallest place with at least left_k tokens of bin_k up to it
-                lo = best, hi = ~0ull;
-                while (lo < hi) {
-                    const unsigned long long mid = lo + (hi - lo) / 2;
-                    count_and_sum(mid, cut.bin_k, cut.bin_k, &n, &w);
-                    if (n >= cut.left_k)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                kept = lo;
-                count_and_sum(kept, cut.bin_k, cut.bin_k, &n, &w);
+                kept = search(cut.bin_k, cut.bin_k, cut.left_k, 0.0, 0ull, lo, hi, &w);
                 all = (double)(cut.sum_before_k + w);
             }
-            if (cut_p) {
-                // the smallest place up to which the weights reach top_p
-                const double want = pp * all;
-                lo = best, hi = kept;
-                while (lo < hi) {
-                    const unsigned long long mid = lo + (hi - lo) / 2;
-                    count_and_sum(mid, cut.lo, cut.hi, &n, &w);
-                    if ((double)(cut.sum_before_lo + w) >= want)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                kept = lo;
-            }
+            if (cut_p) kept = search(cut.lo, cut.hi, 0u, pp * all, cut.sum_before_lo, lo, min(kept, hi), &w);
             last_place = kept;
         }
     }
@@ -1072,7 +1115,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(const SampleParam
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int bin = bin_of(l[j], r);
-                if (bin != kBins - 1 && bin >= cut.sure_end && place_of(l[j], e0 + tid * 4 + j) <= last_place)
+                if (bin != r.last && bin >= cut.sure_end && place_of(l[j], e0 + tid * 4 + j) <= last_place)
                     w += drawn_weight(l[j], bin, r);
             }
             w = wave_sum(w);

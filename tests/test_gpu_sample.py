@@ -119,6 +119,22 @@ def test_ties_and_degenerate_rows():
         check(z.to(BF16), u, t, k, None, None, f"ties bf16 {i}")
 
 
+@pytest.mark.parametrize("V", [152064, 400000])
+def test_deep_cuts(V):
+    # flat rows: cuts deep in the bulk, top-k of tens of thousands, long vocabularies
+    g = torch.Generator().manual_seed(V)
+    z = torch.cat([1.3 * torch.randn(3, V, generator=g), 0.01 * torch.randn(1, V, generator=g)])
+    p = torch.tensor([0.9, 0.5, 0.99, 0.3])
+    k = torch.tensor([0, 60000, 30000, 0], dtype=torch.int32)
+    u = torch.rand(4, generator=g)
+    t = torch.tensor([1.0, 0.7, 1.5, 1.0])
+    check(z, u, t, k, p, None, "deep cuts")
+    check(z, u, t, k, p, torch.full((4,), 0.01), "deep cuts, min-p")
+    check(z, u, None, None, None, torch.full((4,), 1e-5), "min-p below the near weights")
+    check((4 * z).to(BF16), u, t, k, p, None, "deep cuts bf16")
+    check((2 * z).round() / 2, u, t, k, p, None, "a few values, cuts in long runs of equal logits")
+
+
 def test_extreme_settings():
     g = torch.Generator().manual_seed(11)
     z = 3 * torch.randn(8, 5000, generator=g)
