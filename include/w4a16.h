@@ -237,7 +237,7 @@ enum { W4_F32 = 0, W4_BF16 = 1 };
  *   x [M, H], residual [M, H]: W4_F32 or W4_BF16 with row strides >= H; weight [H]: either type.
  *   residual_out [M, H], dense, of the residual's type: r (it may be the residual itself when
  *   that is dense).  Codes and r are reproducible bit for bit.
- *   1 <= H <= 32768; H % 128 == 0 for 8- and 4-bit output; eps >= 0.  Arrays are aligned to
+ *   0 <= M < 2^22, 1 <= H <= 32768; H % 128 == 0 for 8- and 4-bit output; eps >= 0.  Arrays are aligned to
  *   their type (8-bit codes to 8 bytes); H % 8 == 0 with 16-byte aligned rows takes the
  *   vectorized path.
  */
@@ -260,8 +260,8 @@ w4_status w4_act_dequantize(const void *codes, const float *scales, float *out, 
  *                    s = amax_D / 127, code = clamp(rint(x / s), -127, 127), 0 if s == 0;
  *                    it stands for code * s.  binary32 steps with IEEE division, ties to even:
  *                    bit for bit reproducible.
- * A token's place is its slot, page * page_size + offset (int64).  D is 64 or 128, 1 <= page_size
- * <= 65536; caches 16-byte aligned.
+ * A token's place is its slot, page * page_size + offset (int64).  0 <= T < 2^27, D is 64 or 128,
+ * 1 <= page_size <= 65536; caches 16-byte aligned.
  *
  * w4_kv_write puts the keys and values of T tokens into their slots; a token whose slot lies
  * outside [0, pages * page_size) is skipped (padding).  Slots must differ from each other.

@@ -175,9 +175,9 @@ w4_status check_cache(const char *name, int64_t T, int64_t heads, int64_t D, int
         set_error("%s: cache_bits=%d: need 16 or 8", name, cache_bits);
         return W4_ERR_SHAPE;
     }
-    if (T < 0 || T > 0x7FFFFFFF || heads < 1 || heads > 65535 || (D != 64 && D != 128) || pages < 1 ||
+    if (T < 0 || T >= 1 << 27 || heads < 1 || heads > 65535 || (D != 64 && D != 128) || pages < 1 ||
         page_size < 1 || page_size > 65536 || pages > ((int64_t)1 << 40) / (heads * page_size * D)) {
-        set_error("%s: T=%lld heads=%lld D=%lld pages=%lld page_size=%lld: need T>=0, 1<=heads<=65535, D 64 or 128, "
+        set_error("%s: T=%lld heads=%lld D=%lld pages=%lld page_size=%lld: need 0<=T<2^27, 1<=heads<=65535, D 64 or 128, "
                   "pages>=1, 1<=page_size<=65536", name, (long long)T, (long long)heads, (long long)D,
                   (long long)pages, (long long)page_size);
         return W4_ERR_SHAPE;

@@ -24,7 +24,7 @@ NORM = dict(x=P[0], x_type=F32, x_stride=256, res=P[1], res_type=BF16, res_strid
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL), (dict(res_out=None), NULL),
     (dict(bits=8), NULL), (dict(bits=4), NULL),
     (dict(x_type=2), SHAPE), (dict(w_type=-1), SHAPE), (dict(res_type=7), SHAPE), (dict(bits=5), SHAPE),
-    (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(H=0), SHAPE), (dict(H=32769, x_stride=40000, res_stride=40000), SHAPE),
+    (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(M=1 << 22), SHAPE), (dict(H=0), SHAPE), (dict(H=32769, x_stride=40000, res_stride=40000), SHAPE),
     (dict(H=200, bits=8, scales=P[5]), SHAPE), (dict(H=200, bits=4, scales=P[5]), SHAPE),
     (dict(x_stride=255), SHAPE), (dict(res_stride=255), SHAPE), (dict(x_stride=1 << 41), SHAPE),
     (dict(eps=-1.0), SHAPE), (dict(eps=float("nan")), SHAPE),
@@ -55,7 +55,7 @@ READ = dict(slots=P[2], kc=P[3], vc=P[4], ks=P[5], vs=P[6], bits=8, k=P[0], v=P[
             pages=10, page_size=64, stream=None)
 CACHE = [
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(slots=None), NULL), (dict(kc=None), NULL), (dict(vc=None), NULL),
-    (dict(ks=None), NULL), (dict(vs=None), NULL), (dict(bits=4), SHAPE), (dict(T=-1), SHAPE), (dict(heads=0), SHAPE),
+    (dict(ks=None), NULL), (dict(vs=None), NULL), (dict(bits=4), SHAPE), (dict(T=-1), SHAPE), (dict(T=1 << 27), SHAPE), (dict(heads=0), SHAPE),
     (dict(heads=65536), SHAPE), (dict(D=96), SHAPE), (dict(D=256), SHAPE), (dict(pages=0), SHAPE),
     (dict(page_size=0), SHAPE), (dict(page_size=65537), SHAPE), (dict(pages=1 << 40), SHAPE),
     (dict(slots=P[2] + 4), ALIGN), (dict(kc=P[3] + 8), ALIGN), (dict(vc=P[4] + 8), ALIGN), (dict(ks=P[5] + 2), ALIGN),
